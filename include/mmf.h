@@ -76,7 +76,12 @@ typedef enum {
   MMF_OP_STACK = 4,     /* mmf_stack_fwd: m = b*t tokens, d, inner, n_layers      */
   MMF_OP_SCAN = 5,      /* mmf_hgrn_scan: m = b*t tokens, d channels              */
   MMF_OP_HEAD = 6,      /* mmf_lm_head_argmax: inner = vocabulary size            */
-  MMF_OP_BITLINEAR_BWD = 7 /* mmf_bitlinear_backward: m rows, d = K, inner = N     */
+  MMF_OP_BITLINEAR_BWD = 7, /* mmf_bitlinear_backward: m rows, d = K, inner = N     */
+  MMF_OP_RMSNORM_BWD = 8,  /* mmf_rmsnorm_backward: m rows, d                      */
+  /* the head losses: m rows, d, inner = vocabulary size, n_layers = bit 0 set when x is float32 and
+   * bit 1 set when the table is */
+  MMF_OP_HEAD_LOSS = 9,     /* mmf_lm_head_xent_fwd, mmf_lm_head_distill_fwd           */
+  MMF_OP_HEAD_LOSS_BWD = 10 /* mmf_lm_head_xent_backward, mmf_lm_head_distill_backward */
 } mmf_op;
 
 /* A packed ternary weight (device pointers). */
@@ -269,6 +274,78 @@ mmf_status mmf_embed_gather(const int32_t* ids, int64_t m, const void* table, mm
 mmf_status mmf_lm_head_argmax(const void* x, mmf_dtype x_dtype, int32_t b, int32_t d, const float* norm_w,
                               float eps, const void* table, mmf_dtype table_dtype, int32_t vocab,
                               int32_t* ids, float* logits, void* ws, size_t ws_bytes, mmf_stream_t stream);
+
+/* ---- the training end of the tied head (the pages name the training, print no equations) ------ */
+
+/* RMSNorm (the model's final norm, eps 1e-8 as in the blocks; hysenlabs.com block structure):
+ *   y = x rho norm_w, rho = (mean(x^2) + eps)^(-1/2)
+ *   x [m][d] x_dtype; norm_w [d] float32 or NULL (unit gain); y [m][d] y_dtype; eps >= 0, any d >= 1.
+ * Float32 sums, one rounding to y's type. Rows with 16-byte aligned buffers and d a multiple of 8 up
+ * to 16384 are read once; others through a general kernel that reads them twice. m = 0 is a no-op. */
+mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
+                           void* y, mmf_dtype y_dtype, mmf_stream_t stream);
+
+/* Its gradients: u = dy norm_w, dx = rho u - rho^3 x mean(u x), dnorm_w[c] = sum_r dy[r][c] x[r][c] rho_r.
+ *   x [m][d] x_dtype; dy [m][d] dy_dtype; dx [m][d] x_dtype out; dnorm_w [d] float32 out or NULL.
+ *   ws >= mmf_workspace_bytes(MMF_OP_RMSNORM_BWD, m, d, 0, 0) when dnorm_w is asked for.
+ * Float32 sums in a fixed order (deterministic). m = 0 writes a zero dnorm_w. */
+mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
+                                const void* dy, mmf_dtype dy_dtype, void* dx, float* dnorm_w, void* ws,
+                                size_t ws_bytes, mmf_stream_t stream);
+
+/* Softmax cross entropy of the tied head, without the logits ever being stored:
+ *   s_rv = sum_k x[r][k] table[v][k];  lse[r] = log sum_v exp(s_rv);  loss[r] = lse[r] - s_r,targets[r]
+ *   x       [m][d] x_dtype, 16-byte aligned: the normalised hidden rows (mmf_rmsnorm_fwd's y);
+ *           d a multiple of 8, 8 to 32768; 0 <= m <= 2^30.
+ *   table   [vocab][d] table_dtype, 16-byte aligned (the embedding table); 1 <= vocab <= 2^30.
+ *   targets [m] int32. A target outside [0, vocab) leaves its row out: loss = lse = 0, and nothing of
+ *           that row is computed with (it may hold anything).
+ *   loss, lse [m] float32 out. Sums and mean over the rows are the caller's.
+ *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, type bits). m = 0 is a no-op.
+ * bf16 tensor cores with float32 accumulation and softmax statistics; a float32 operand enters as
+ * three bf16 planes that hold it exactly, so float32 inputs give float32-accurate results.
+ * Deterministic. */
+mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, float* loss, float* lse,
+                                void* ws, size_t ws_bytes, mmf_stream_t stream);
+
+/* Its gradients, from the forward's lse and dloss [m] float32 (dL/dloss; a mean over rows is
+ * dloss = 1 / rows):  g_rv = dloss[r] (exp(s_rv - lse[r]) - [v = targets[r]])
+ *   dx = g table          [m][d] x_dtype out or NULL, 16-byte aligned (zero in rows left out)
+ *   dtable = g^T x        [vocab][d] table_dtype out or NULL, 16-byte aligned (every row written)
+ * The logits are computed again in pieces of the vocabulary; one piece's g is held in the workspace
+ * (about 512 MB at most up to 65536 rows). g is rounded to bf16 once where x and table are bf16, and
+ * kept as three exact planes otherwise; both products accumulate in float32.
+ *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, type bits). m = 0 zeroes dtable. */
+mmf_status mmf_lm_head_xent_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                     mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, const float* lse,
+                                     const float* dloss, void* dx, void* dtable, void* ws, size_t ws_bytes,
+                                     mmf_stream_t stream);
+
+/* Distillation of the tied head from a teacher's top_k logits per row, without storing the logits:
+ *   an entry j of row r is valid when t_ids[r][j] is in [0, vocab) and t_logits[r][j] > -inf;
+ *   q_rj = softmax over the row's valid entries of t_logits[r][j] / temperature
+ *   lse[r] = log sum_v exp(s_rv / temperature)                     (s as in mmf_lm_head_xent_fwd)
+ *   loss[r] = sum_j q_rj (log q_rj - s_r,t_ids[r][j] / temperature + lse[r])      (0 log 0 = 0)
+ *   t_ids [m][top_k] int32; t_logits [m][top_k] t_dtype; 1 <= top_k <= 256; 1e-3 <= temperature <= 1e3.
+ *   loss, lse [m] float32 out; s_top [m][top_k] float32 out: the student's logits at the teacher's
+ *   ids (0 for entries that are not valid), which the backward takes.
+ * A row with no valid entry is left out as a row without target is (zeros). Entries of one row may
+ * name one id; their q add up in the gradient. The factor temperature^2 some use is the caller's.
+ *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, type bits). m = 0 is a no-op. */
+mmf_status mmf_lm_head_distill_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                   mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids, const void* t_logits,
+                                   mmf_dtype t_dtype, int32_t top_k, float temperature, float* loss, float* lse,
+                                   float* s_top, void* ws, size_t ws_bytes, mmf_stream_t stream);
+
+/* Its gradients: g_rv = dloss[r] / temperature (exp(s_rv / temperature - lse[r]) - sum_{j: id = v} q_rj),
+ * dx = g table, dtable = g^T x as above (the teacher's entries are computed whole in float32 before
+ * their one rounding).  ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, type bits). */
+mmf_status mmf_lm_head_distill_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                        mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids,
+                                        const void* t_logits, mmf_dtype t_dtype, int32_t top_k, float temperature,
+                                        const float* lse, const float* s_top, const float* dloss, void* dx,
+                                        void* dtable, void* ws, size_t ws_bytes, mmf_stream_t stream);
 
 /* Integrity check of a packed ternary matrix (the format above): *bad (device, 8-byte aligned)
  * receives the number of malformed 2-bit fields: fields of real columns holding the unused

@@ -10,6 +10,7 @@ C entry points are available as ``lib().mmf_*``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass, field
@@ -22,7 +23,7 @@ LIB_PATH = os.path.join(_HERE, "libmmf.so")
 MMF_OK, MMF_ERR_INVALID_ARG, MMF_ERR_UNSUPPORTED, MMF_ERR_WORKSPACE, MMF_ERR_CUDA, MMF_ERR_TIMEOUT = range(6)
 MMF_F32, MMF_BF16 = 0, 1
 (MMF_OP_PACK, MMF_OP_BITLINEAR, MMF_OP_BLOCK, MMF_OP_DECODE, MMF_OP_STACK, MMF_OP_SCAN, MMF_OP_HEAD,
- MMF_OP_BITLINEAR_BWD) = range(8)
+ MMF_OP_BITLINEAR_BWD, MMF_OP_RMSNORM_BWD, MMF_OP_HEAD_LOSS, MMF_OP_HEAD_LOSS_BWD) = range(11)
 MMF_GEMM_AUTO, MMF_GEMM_TENSOR, MMF_GEMM_SIMT = range(3)
 MMF_DECODE_AUTO, MMF_DECODE_FUSED, MMF_DECODE_SKINNY, MMF_DECODE_BLOCK = range(4)
 
@@ -34,6 +35,8 @@ EXPORTED = (
     "mmf_stack_fwd", "mmf_sync_status", "mmf_status_string", "mmf_last_error",
     "mmf_set_gemm_path", "mmf_set_wait_limit", "mmf_launch_count", "mmf_timing_enable", "mmf_timing_read",
     "mmf_bitlinear_fwd_noalloc", "mmf_decode_step_taps", "mmf_set_decode_path", "mmf_decode_path_for",
+    "mmf_rmsnorm_fwd", "mmf_rmsnorm_backward", "mmf_lm_head_xent_fwd", "mmf_lm_head_xent_backward",
+    "mmf_lm_head_distill_fwd", "mmf_lm_head_distill_backward",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -111,6 +114,18 @@ def lib() -> ctypes.CDLL:
                                                   vp, vp, vp, ctypes.c_int, vp, vp, vp, vp, sz, st]),
         "mmf_stack_fwd": (ctypes.c_int, [ctypes.POINTER(BlockWeightsC), i32, vp, i32, i64, vp, i32,
                                          ctypes.c_int, vp, vp, vp, sz, st]),
+        "mmf_rmsnorm_fwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, vp, ctypes.c_float, vp, ctypes.c_int, st]),
+        "mmf_rmsnorm_backward": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, vp, ctypes.c_float, vp, ctypes.c_int, vp,
+                                                vp, vp, sz, st]),
+        "mmf_lm_head_xent_fwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, vp, ctypes.c_int, i32, vp, vp, vp, vp, sz,
+                                                st]),
+        "mmf_lm_head_xent_backward": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, vp, ctypes.c_int, i32, vp, vp, vp, vp,
+                                                     vp, vp, sz, st]),
+        "mmf_lm_head_distill_fwd": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, vp, ctypes.c_int, i32, vp, vp,
+                                                   ctypes.c_int, i32, ctypes.c_float, vp, vp, vp, vp, sz, st]),
+        "mmf_lm_head_distill_backward": (ctypes.c_int, [vp, ctypes.c_int, i64, i32, vp, ctypes.c_int, i32, vp, vp,
+                                                        ctypes.c_int, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, sz,
+                                                        st]),
         "mmf_sync_status": (ctypes.c_int, [st]),
         "mmf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "mmf_last_error": (ctypes.c_char_p, []),
@@ -182,6 +197,11 @@ def _i32(t: torch.Tensor, name: str) -> torch.Tensor:
 
 def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(device: torch.device):
+    """The library launches on the current device: make it the tensors' (nothing to do off the GPU)."""
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
 
 
 _ws_cache: dict[tuple[int, int], torch.Tensor] = {}
@@ -568,6 +588,165 @@ def lm_head_argmax(x: torch.Tensor, norm_w: torch.Tensor | None, table: torch.Te
                                     logits.data_ptr() if logits is not None else None, ws.data_ptr(), ws.numel(),
                                     _stream(x.device)), "mmf_lm_head_argmax")
     return (ids, logits) if want_logits else ids
+
+
+# ---------------------------------------------------------------------------------------------
+# the training end of the tied head
+# ---------------------------------------------------------------------------------------------
+def _scratch(op: int, m: int, d: int, inner: int, bits: int, device: torch.device) -> torch.Tensor:
+    """A scratch buffer of this call's own: PyTorch's allocator orders its reuse on the current stream
+    and keeps it with the graph when the call is being captured, so that no two graphs, streams or
+    calls share one."""
+    need = int(lib().mmf_workspace_bytes(op, m, d, inner, bits))
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
+def _together(first: torch.Tensor, **others: torch.Tensor | None) -> None:
+    """Every tensor of a call has to be on one device."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name}: on {t.device}, expected {first.device}")
+
+
+def rmsnorm_fwd(x: torch.Tensor, norm_w: torch.Tensor | None, eps: float = 1e-8,
+                y_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """mmf_rmsnorm_fwd on x [..., d]: y = x / sqrt(mean(x^2) + eps) * norm_w, in y_dtype (x's by
+    default)."""
+    _dev(x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x: expected [..., d], got {tuple(x.shape)}")
+    d = x.shape[-1]
+    _f32(norm_w, (d,), "norm_w")
+    _together(x, norm_w=norm_w)
+    y = torch.empty(x.shape, dtype=y_dtype or x.dtype, device=x.device)
+    with _on(x.device):
+        _check(lib().mmf_rmsnorm_fwd(x.data_ptr(), _dt(x.dtype), x.numel() // d, d, _ptr(norm_w), eps, y.data_ptr(),
+                                     _dt(y.dtype), _stream(x.device)), "mmf_rmsnorm_fwd")
+    return y
+
+
+def rmsnorm_backward(x: torch.Tensor, norm_w: torch.Tensor | None, dy: torch.Tensor, eps: float = 1e-8,
+                     want_dnorm_w: bool = True):
+    """mmf_rmsnorm_backward: (dx in x's dtype, dnorm_w [d] float32 or None) from x and dy [..., d]."""
+    _dev(x)
+    _dev(dy)
+    if x.dim() < 1 or x.shape[-1] < 1 or dy.shape != x.shape:
+        raise ValueError(f"x and dy need one shape [..., d], got {tuple(x.shape)} and {tuple(dy.shape)}")
+    d = x.shape[-1]
+    m = x.numel() // d
+    _f32(norm_w, (d,), "norm_w")
+    _together(x, norm_w=norm_w, dy=dy)
+    dx = torch.empty_like(x)
+    dnw = torch.empty(d, dtype=torch.float32, device=x.device) if want_dnorm_w else None
+    with _on(x.device):
+        ws = _scratch(MMF_OP_RMSNORM_BWD, m, d, 0, 0, x.device)
+        _check(lib().mmf_rmsnorm_backward(x.data_ptr(), _dt(x.dtype), m, d, _ptr(norm_w), eps, dy.data_ptr(),
+                                          _dt(dy.dtype), dx.data_ptr(), _ptr(dnw), ws.data_ptr(), ws.numel(),
+                                          _stream(x.device)), "mmf_rmsnorm_backward")
+    return dx, dnw
+
+
+def _head_loss_args(x: torch.Tensor, table: torch.Tensor) -> tuple[int, int, int, int]:
+    _dev(x)
+    _dev(table)
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [m, d], got {tuple(x.shape)}")
+    m, d = x.shape
+    if table.dim() != 2 or table.shape[1] != d:
+        raise ValueError(f"table: expected [vocab, {d}], got {tuple(table.shape)}")
+    _together(x, table=table)
+    return m, d, table.shape[0], (1 if _dt(x.dtype) == MMF_F32 else 0) | (2 if _dt(table.dtype) == MMF_F32 else 0)
+
+
+def _teacher_args(x: torch.Tensor, t_ids: torch.Tensor, t_logits: torch.Tensor) -> int:
+    _i32(t_ids, "t_ids")
+    _dev(t_logits)
+    if t_ids.dim() != 2 or t_ids.shape[0] != x.shape[0] or t_logits.shape != t_ids.shape:
+        raise ValueError(f"t_ids, t_logits: expected one shape [{x.shape[0]}, top_k], got {tuple(t_ids.shape)} and "
+                         f"{tuple(t_logits.shape)}")
+    _together(x, t_ids=t_ids, t_logits=t_logits)
+    return t_ids.shape[1]
+
+
+def lm_head_xent_fwd(x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor):
+    """mmf_lm_head_xent_fwd: (loss [m], lse [m]) float32 of normalised rows x [m, d] against the tied
+    table [vocab, d] and int32 targets [m]; a target outside [0, vocab) leaves its row out (zeros)."""
+    m, d, vocab, bits = _head_loss_args(x, table)
+    if tuple(_i32(targets, "targets").shape) != (m,):
+        raise ValueError(f"targets: expected [{m}], got {tuple(targets.shape)}")
+    _together(x, targets=targets)
+    loss = torch.empty(m, dtype=torch.float32, device=x.device)
+    lse = torch.empty(m, dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        ws = _scratch(MMF_OP_HEAD_LOSS, m, d, vocab, bits, x.device)
+        _check(lib().mmf_lm_head_xent_fwd(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(), _dt(table.dtype), vocab,
+                                          targets.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                                          ws.numel(), _stream(x.device)), "mmf_lm_head_xent_fwd")
+    return loss, lse
+
+
+def lm_head_xent_backward(x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                          dloss: torch.Tensor, want_dx: bool = True, want_dtable: bool = True):
+    """mmf_lm_head_xent_backward: (dx [m, d] or None, dtable [vocab, d] or None), in x's and the
+    table's dtype, from the forward's lse and dloss [m] float32 (dL/dloss)."""
+    m, d, vocab, bits = _head_loss_args(x, table)
+    if tuple(_i32(targets, "targets").shape) != (m,):
+        raise ValueError(f"targets: expected [{m}], got {tuple(targets.shape)}")
+    _f32(lse, (m,), "lse")
+    _f32(dloss, (m,), "dloss")
+    _together(x, targets=targets, lse=lse, dloss=dloss)
+    dx = torch.empty_like(x) if want_dx else None
+    dtable = torch.empty_like(table) if want_dtable else None
+    with _on(x.device):
+        ws = _scratch(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, bits, x.device)
+        _check(lib().mmf_lm_head_xent_backward(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(), _dt(table.dtype),
+                                               vocab, targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), _ptr(dx),
+                                               _ptr(dtable), ws.data_ptr(), ws.numel(), _stream(x.device)),
+               "mmf_lm_head_xent_backward")
+    return dx, dtable
+
+
+def lm_head_distill_fwd(x: torch.Tensor, table: torch.Tensor, t_ids: torch.Tensor, t_logits: torch.Tensor,
+                        temperature: float = 1.0):
+    """mmf_lm_head_distill_fwd: (loss [m], lse [m], s_top [m, top_k]) float32 of normalised rows x
+    [m, d] against the tied table and a teacher's top logits (t_ids int32, t_logits, both [m, top_k]).
+    Entries with an id outside [0, vocab) or a logit of -inf do not count."""
+    m, d, vocab, bits = _head_loss_args(x, table)
+    k = _teacher_args(x, t_ids, t_logits)
+    loss = torch.empty(m, dtype=torch.float32, device=x.device)
+    lse = torch.empty(m, dtype=torch.float32, device=x.device)
+    s_top = torch.empty(m, k, dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        ws = _scratch(MMF_OP_HEAD_LOSS, m, d, vocab, bits, x.device)
+        _check(lib().mmf_lm_head_distill_fwd(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(), _dt(table.dtype),
+                                             vocab, t_ids.data_ptr(), t_logits.data_ptr(), _dt(t_logits.dtype), k,
+                                             temperature, loss.data_ptr(), lse.data_ptr(), s_top.data_ptr(),
+                                             ws.data_ptr(), ws.numel(), _stream(x.device)), "mmf_lm_head_distill_fwd")
+    return loss, lse, s_top
+
+
+def lm_head_distill_backward(x: torch.Tensor, table: torch.Tensor, t_ids: torch.Tensor, t_logits: torch.Tensor,
+                             lse: torch.Tensor, s_top: torch.Tensor, dloss: torch.Tensor, temperature: float = 1.0,
+                             want_dx: bool = True, want_dtable: bool = True):
+    """mmf_lm_head_distill_backward: (dx [m, d] or None, dtable [vocab, d] or None), in x's and the
+    table's dtype, from the forward's lse and s_top and dloss [m] float32 (dL/dloss)."""
+    m, d, vocab, bits = _head_loss_args(x, table)
+    k = _teacher_args(x, t_ids, t_logits)
+    _f32(lse, (m,), "lse")
+    _f32(s_top, (m, k), "s_top")
+    _f32(dloss, (m,), "dloss")
+    _together(x, lse=lse, s_top=s_top, dloss=dloss)
+    dx = torch.empty_like(x) if want_dx else None
+    dtable = torch.empty_like(table) if want_dtable else None
+    with _on(x.device):
+        ws = _scratch(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, bits, x.device)
+        _check(lib().mmf_lm_head_distill_backward(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(),
+                                                  _dt(table.dtype), vocab, t_ids.data_ptr(), t_logits.data_ptr(),
+                                                  _dt(t_logits.dtype), k, temperature, lse.data_ptr(),
+                                                  s_top.data_ptr(), dloss.data_ptr(), _ptr(dx), _ptr(dtable),
+                                                  ws.data_ptr(), ws.numel(), _stream(x.device)),
+               "mmf_lm_head_distill_backward")
+    return dx, dtable
 
 
 def stack_fwd(blocks: list[Block], ids: torch.Tensor, table: torch.Tensor, want_state: bool = False,

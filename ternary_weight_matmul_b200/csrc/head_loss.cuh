@@ -1,0 +1,928 @@
+// head_loss.cuh -- K15: losses over the tied head's vocabulary without keeping the logits: softmax
+// cross entropy and distillation from a teacher's top logits, forward and backward.
+//
+// With the normalised hidden rows x [m][d] and the table T [vocab][d], s = x T^T:
+//   forward   lse_r = log sum_v exp(s_rv / tau): logits tiles live in tensor memory only; each tile
+//             leaves one (maximum, sum) pair per row, and a small kernel joins the pairs of a row.
+//   backward  g_rv = c_r (exp(s_rv / tau - lse_r) - teacher_rv), dx = g T, dT = g^T x, in pieces of
+//             the vocabulary: one launch recomputes a piece's logits and writes its g (bf16), one
+//             launch forms both products from it. Nothing of size m x vocab is kept.
+// Rows without a target are left out before any product: a scan lists the live rows, a gather copies
+// them together, and every kernel reads the live count on the device (no host synchronisation, and
+// what a dropped row holds, NaN included, reaches nothing).
+//
+// All three products are one warp-specialised tcgen05 kernel: a TMA producer thread, an MMA thread,
+// eight epilogue warps, persistent over tiles, two accumulators in tensor memory so that a tile's
+// epilogue runs under the next tile's MMAs. Operands are bf16; a float32 operand enters as three
+// bf16 planes that add up to it exactly (8 + 8 + 8 significant bits, by truncation), and a product
+// of float32 accuracy runs over the plane pairs (i, j) with i + j <= 2, smallest terms first.
+//
+// The tensor cores' float32 accumulator cuts bits off at every step of K = 16, towards zero: a bias of
+// about half an ulp of the running sum per step, 1.3e-6 of logits of size 2 at d = 1024 and 3.8e-6 at
+// 2560 (a float32 sum on the CUDA cores: below 1e-9). Where a result is kept in float32 (the loss
+// statistics, and every gradient with a float32 operand) the kernel therefore starts a new accumulator
+// every FLUSH_KB k-blocks and the epilogue adds the pieces in registers, rounding to nearest.
+#pragma once
+
+#include "common.cuh"
+
+namespace mmf {
+namespace hl {
+
+constexpr int BM = 128;        // rows of D per tile (MMA M)
+constexpr int BN = 256;        // columns of D per tile (MMA N)
+constexpr int BK = 64;         // bf16 per k-block: one 128-byte swizzle atom
+constexpr int UK = 16;         // K per kind::f16 instruction
+constexpr int STAGES = 4;
+constexpr int FLUSH_KB = 4;    // k-blocks per accumulator where pieces are added in registers
+constexpr int BOX_BYTES = 64 * BK * 2;  // every TMA load box: 64 x 64 bf16, 8 KB
+constexpr int A_BOXES = BM / 64, B_BOXES = BN / 64;
+constexpr int STAGE_BYTES = (A_BOXES + B_BOXES) * BOX_BYTES;
+constexpr int EPI_WARPS = 8;   // two per tensor-memory lane quarter, each half of the columns
+constexpr int THREADS = (4 + EPI_WARPS) * 32;
+constexpr int OUT_BYTES = 4096;  // staging per epilogue warp: 32 rows x 128 bytes
+constexpr int NUM_BARS = 2 * STAGES + 5;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES + NUM_BARS * 8 + 16;
+constexpr uint32_t TMEM_COLS = 2 * BN;
+constexpr int PLANES = 3;      // bf16 planes of a float32 operand
+constexpr int MAX_PRODS = 6;
+constexpr int MAX_TOP = 256;   // teacher entries per row
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
+enum Mode : int { kStats = 0, kGrad = 1, kProducts = 2 };
+
+// Plane pairs of one product, smallest terms first.
+struct Prods {
+  int32_t n;
+  uint8_t a[MAX_PRODS], b[MAX_PRODS];
+};
+
+struct Params {
+  CUtensorMap x;    // live rows, planes   [px][m_pad][d] bf16, box 64 x 64 (all loads)
+  CUtensorMap t;    // table, planes       [pt][vocab][d] bf16
+  CUtensorMap g;    // the piece's g       [pg][m_pad][ldg] bf16, inner extent = piece columns; one plane
+                    // rounded to nearest, or with FLUSH three that split it exactly
+  CUtensorMap g_out;   // the same array, box 64 x 32 (stores)
+  CUtensorMap dx_out;  // float32 partials [planes][m_pad][d], box 32 x 32
+  CUtensorMap dt_out;  // dtable's rows of the piece (its dtype), or float32 partials [planes][vocab][d]
+  const int32_t* live;  // device: live rows
+  int32_t d, vocab;
+  int32_t v0, vn;       // vocabulary range of this launch
+  int64_t m_pad;
+  float scale;          // log2(e) / tau
+  const int32_t* tgt;   // [m_pad] target of each live row, or nullptr (kStats, kGrad)
+  const float* lse;     // [m_pad] (kGrad)
+  const float* c;       // [m_pad] dloss / tau (kGrad)
+  float2* part;         // [2 * column tiles][m_pad] (maximum, sum) (kStats)
+  float* st;            // [m_pad] target logit (kStats)
+  Prods fwd, dxp, dtp;
+  int32_t dx_split, dx_plane0;  // K splits of dx in this launch (0: no dx) and its first partial plane
+  int32_t dt_split;             // K splits of dT (0: no dT)
+  int32_t dt_f32;               // dt_out holds float32
+  int32_t dt_row0;              // first row of dt_out this launch writes
+  uint32_t wait_limit_us;
+};
+
+// ---------------------------------------------------------------------------------------------
+// PTX used here only
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// 2^v by the hardware approximation (2 ulp over the range the softmax needs; 0 for -inf).
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// Shared-memory descriptor of an MN-major, 128-byte-swizzled operand: atoms of 64 MN elements (128
+// bytes) x 8 k rows. Leading byte offset = the next 64 MN elements (one box), stride byte offset =
+// the next 8 k rows.
+__device__ __forceinline__ uint64_t mn128_desc(uint32_t smem_addr) {
+  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(BOX_BYTES >> 4) << 16) | ((uint64_t)64u << 32) |
+         ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// x = p0 + p1 + p2 exactly: each plane keeps the 8 leading significant bits of what is left
+// (truncation never overflows). An infinity or NaN stays whole in the first plane.
+__device__ __forceinline__ float trunc_bf16(float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); }
+// Takes the leading plane off v and leaves the rest.
+__device__ __forceinline__ float peel(float& v) {
+  const bool finite = (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u;
+  const float p = v != v ? __uint_as_float(0x7fc00000u) : trunc_bf16(v);
+  v = finite ? v - p : 0.0f;
+  return p;
+}
+__device__ __forceinline__ void split3(float v, float& p0, float& p1, float& p2) {
+  p0 = peel(v);
+  p1 = peel(v);
+  p2 = peel(v);
+}
+__device__ __forceinline__ uint32_t pack_bf16_rn(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+// two values that are exact in bf16
+__device__ __forceinline__ uint32_t pack_bf16_hi(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+// ---------------------------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------------------------
+struct Tile {
+  int row, col;     // first row / column of D
+  int kb0, nkb;     // k-blocks (per plane pair)
+  int nprod;
+  int kind;         // kProducts: 0 = dT, 1 = dx; else 0
+  int split;
+};
+
+__host__ __device__ __forceinline__ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <int MODE>
+__device__ __forceinline__ int tile_count(const Params& P, int live) {
+  if (MODE != kProducts) return cdiv(live, BM) * cdiv(P.vn, BN);
+  return P.dt_split * cdiv(P.vn, BM) * cdiv(P.d, BN) + P.dx_split * cdiv(live, BM) * cdiv(P.d, BN);
+}
+
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(const Params& P, int live, int t) {
+  Tile T;
+  T.kind = 0;
+  T.split = 0;
+  if (MODE != kProducts) {
+    // groups of row tiles, columns slow inside a group: the CTAs of one wave share a few row tiles
+    // and a few table tiles, which the L2 then serves
+    constexpr int G = 16;
+    const int mt = cdiv(live, BM), nt = cdiv(P.vn, BN);
+    const int grp = t / (G * nt), rem = t - grp * (G * nt);
+    const int gm = mt - grp * G < G ? mt - grp * G : G;
+    T.row = (grp * G + rem % gm) * BM;
+    T.col = (rem / gm) * BN;
+    T.kb0 = 0;
+    T.nkb = cdiv(P.d, BK);
+    T.nprod = P.fwd.n;
+    return T;
+  }
+  const int nt = cdiv(P.d, BN);
+  const int per_dt = cdiv(P.vn, BM) * nt, per_dx = cdiv(live, BM) * nt;
+  int kb, splits, rem;
+  if (t < P.dt_split * per_dt) {
+    T.split = t / per_dt;
+    rem = t - T.split * per_dt;
+    kb = cdiv(live, BK);
+    splits = P.dt_split;
+    T.nprod = P.dtp.n;
+  } else {
+    t -= P.dt_split * per_dt;
+    T.kind = 1;
+    T.split = t / per_dx;
+    rem = t - T.split * per_dx;
+    kb = cdiv(P.vn, BK);
+    splits = P.dx_split;
+    T.nprod = P.dxp.n;
+  }
+  T.row = (rem / nt) * BM;
+  T.col = (rem % nt) * BN;
+  const int per = cdiv(kb, splits);
+  T.kb0 = T.split * per;
+  T.nkb = kb - T.kb0 < per ? kb - T.kb0 : per;
+  if (T.nkb < 0) T.nkb = 0;
+  return T;
+}
+
+// ---------------------------------------------------------------------------------------------
+// the product kernel
+// ---------------------------------------------------------------------------------------------
+// accumulators (segments of K) of a tile
+template <bool FLUSH>
+__device__ __forceinline__ int tile_segments(const Tile& T) {
+  const int total = T.nprod * T.nkb;
+  return FLUSH && total > FLUSH_KB ? cdiv(total, FLUSH_KB) : 1;
+}
+
+template <int MODE, bool FLUSH>
+__global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_constant__ Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + STAGES * STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI_WARPS * OUT_BYTES);
+  uint64_t* full = bars;                     // TMA -> MMA           (count 1 + tx bytes)
+  uint64_t* empty = bars + STAGES;           // MMA commit -> TMA    (count 1)
+  uint64_t* accfull = bars + 2 * STAGES;     // MMA commit -> epilogue, two accumulators
+  uint64_t* accempty = accfull + 2;          // epilogue -> MMA      (count EPI_WARPS)
+  uint64_t* drain = accempty + 2;            // MMA drain after an abort
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t limit = P.wait_limit_us;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&accfull[b], 1);
+      mbar_init(&accempty[b], EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 2) tmem_alloc(tmem_slot, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int live = *P.live;
+  const int tiles = tile_count<MODE>(P, live);
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const Tile T = tile_at<MODE>(P, live, t);
+        const Prods& pr = MODE != kProducts ? P.fwd : T.kind ? P.dxp : P.dtp;
+        for (int p = 0; ok && p < T.nprod; ++p) {
+          const int pa = pr.a[p], pb = pr.b[p];
+          for (int kb = 0; kb < T.nkb; ++kb, ++it) {
+            const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+            if (!mbar_wait_bounded(&empty[s], ph ^ 1u, limit, abort_flag)) { ok = false; break; }
+            const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BOXES * BOX_BYTES;
+            const int k = (T.kb0 + kb) * BK;
+            mbar_arrive_expect_tx(&full[s], STAGE_BYTES);
+            if (MODE != kProducts) {
+#pragma unroll
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, T.row + 64 * i, pa, &full[s]);
+#pragma unroll
+              for (int i = 0; i < B_BOXES; ++i)
+                tma_load_3d(sb + i * BOX_BYTES, &P.t, k, P.v0 + T.col + 64 * i, pb, &full[s]);
+            } else if (T.kind == 0) {  // dT = g^T x: both operands MN-major, k = live rows
+#pragma unroll
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, T.row + 64 * i, k, pa, &full[s]);
+#pragma unroll
+              for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.x, T.col + 64 * i, k, pb, &full[s]);
+            } else {  // dx = g T: A K-major, B MN-major, k = vocabulary
+#pragma unroll
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, k, T.row + 64 * i, pa, &full[s]);
+#pragma unroll
+              for (int i = 0; i < B_BOXES; ++i)
+                tma_load_3d(sb + i * BOX_BYTES, &P.t, T.col + 64 * i, P.v0 + k, pb, &full[s]);
+            }
+          }
+        }
+      }
+      if (!ok) {
+        // drain: the stages armed in the last STAGES iterations must see their copies land
+        for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
+          mbar_wait_drain(&full[j % STAGES], (j / STAGES) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      // kind::f16: D float32 (bits 4-5 = 1), A and B bf16 (bits 7-9, 10-12 = 1), MN-major A / B at
+      // bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28
+      constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
+                                  ((uint32_t)(BM >> 4) << 24);
+      uint32_t it = 0, n = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+        const Tile T = tile_at<MODE>(P, live, t);
+        const bool a_mn = MODE == kProducts && T.kind == 0, b_mn = MODE == kProducts;
+        const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        const int total = T.nprod * T.nkb, segs = tile_segments<FLUSH>(T);
+        for (int g = 0; ok && g < segs; ++g, ++n) {
+          const uint32_t buf = n & 1u, acc = tmem + buf * BN;
+          if (!mbar_wait_bounded(&accempty[buf], ((n >> 1) & 1u) ^ 1u, limit, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const int its = !FLUSH ? total : total - g * FLUSH_KB < FLUSH_KB ? total - g * FLUSH_KB : FLUSH_KB;
+          for (int i = 0; i < its; ++i, ++it) {
+            const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+            if (!mbar_wait_bounded(&full[s], ph, limit, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BOXES * BOX_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < BK / UK; ++kk) {
+              const uint64_t ad = a_mn ? mn128_desc(sa + kk * UK * 128) : sw128_desc(sa + kk * UK * 2);
+              const uint64_t bd = b_mn ? mn128_desc(sb + kk * UK * 128) : sw128_desc(sb + kk * UK * 2);
+              tc_mma_bf16_ss(acc, ad, bd, idesc, (i | kk) != 0 ? 1u : 0u);
+            }
+            tc_commit(&empty[s]);
+          }
+          if (ok) tc_commit(&accfull[buf]);
+        }
+      }
+      // everything issued has completed before this thread reaches the teardown barrier
+      tc_commit(drain);
+      mbar_wait_drain(drain, 0u);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t stg = smem_u32(staging + (warp - 4) * OUT_BYTES);
+    const uint32_t swz = (uint32_t)(lane & 7) << 4, stg_row = stg + lane * 128;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile T = tile_at<MODE>(P, live, t);
+      const int row0 = T.row + quarter * 32, row = row0 + lane;
+      const int col0 = T.col + half * (BN / 2);
+      const bool zero = T.nprod * T.nkb == 0;  // no k-blocks: the accumulator was never written
+      uint32_t acc = 0;
+      float sum[FLUSH ? BN / 2 : 1];
+      const int segs = tile_segments<FLUSH>(T);
+#pragma unroll 1
+      for (int g = 0; g < segs; ++g, ++n) {
+        const uint32_t buf = n & 1u;
+        const bool have = mbar_wait_bounded(&accfull[buf], (n >> 1) & 1u, limit, abort_flag);
+        if (!__all_sync(0xffffffffu, have)) { ok = false; break; }
+        tc_fence_after();
+        acc = tmem + buf * BN + half * (BN / 2) + ((uint32_t)(quarter * 32) << 16);
+        if (FLUSH) {
+#pragma unroll
+          for (int c0 = 0; c0 < BN / 2; c0 += 16) {
+            uint32_t w[16];
+            tmem_ld_32x32b_x16(acc + c0, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              sum[c0 + e] = (g == 0 ? 0.0f : sum[c0 + e]) + __uint_as_float(w[e]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&accempty[buf]);
+        }
+      }
+      if (!ok) break;
+      if (FLUSH && zero) {
+#pragma unroll
+        for (int e = 0; e < (FLUSH ? BN / 2 : 1); ++e) sum[e] = 0.0f;
+      }
+      // columns [c0, c0 + N) of D into v (with FLUSH they are in `sum` already)
+      const auto cols32 = [&](int c0, float* v) {
+        uint32_t w[32];
+        tmem_ld_32x32b_x32(acc + c0, w);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = zero ? 0.0f : __uint_as_float(w[e]);
+      };
+      if (MODE == kStats) {
+        constexpr int W = FLUSH ? BN / 2 : 1;  // kStats always runs with FLUSH
+        const int left = P.vn - col0;
+        if (left < W) {
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            if (e >= left) sum[e] = -INFINITY;
+        }
+        const int tgt = P.tgt && row < live ? P.tgt[row] - P.v0 - col0 : -1;
+        if ((uint32_t)tgt < (uint32_t)W) {
+          float hit = 0.0f;
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            if (tgt == e) hit = sum[e];
+          P.st[row] = hit;
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < W; ++e) m4[e & 3] = fmaxf(m4[e & 3], sum[e]);
+        const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const float off = top == -INFINITY ? 0.0f : -top * P.scale;
+#pragma unroll
+        for (int e = 0; e < W; ++e) s4[e & 3] += ex2(fmaf(sum[e], P.scale, off));
+        if (row < live)
+          P.part[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+      } else if (MODE == kGrad) {
+        // pad rows have c = lse = 0: zeros, which the products over the live rows rely on
+        const float c = P.c[row], lse2 = P.lse[row] * kLog2e;
+        const int tgt = P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
+        const auto grads = [&](float* gv, int c0, int w) {
+#pragma unroll
+          for (int e = 0; e < w; ++e) gv[e] = ex2(fmaf(gv[e], P.scale, -lse2));
+          if ((uint32_t)(tgt - c0) < (uint32_t)w) {
+#pragma unroll
+            for (int e = 0; e < w; ++e)
+              if (tgt - c0 == e) gv[e] -= 1.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < w; ++e) gv[e] *= c;
+        };
+        if (FLUSH) grads(sum, 0, FLUSH ? BN / 2 : 0);
+#pragma unroll
+        for (int c0 = 0; c0 < BN / 2; c0 += 64) {
+          if (col0 + c0 >= P.vn) break;
+          float own[FLUSH ? 1 : 64];
+          float* gv = FLUSH ? sum + (FLUSH ? c0 : 0) : own;
+          if (!FLUSH) {
+            cols32(c0, gv);
+            cols32(c0 + 32, gv + 32);
+            grads(gv, c0, FLUSH ? 0 : 64);
+          }
+#pragma unroll
+          for (int p = 0; p < (FLUSH ? PLANES : 1); ++p) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                float& a = gv[8 * j + 2 * q];
+                float& b = gv[8 * j + 2 * q + 1];
+                // keeps the compiler from splitting all values ahead of the stores, into spills
+                asm volatile("" : "+f"(a), "+f"(b));
+                w[q] = FLUSH ? pack_bf16_hi(peel(a), peel(b)) : pack_bf16_rn(a, b);
+              }
+              st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), w[0], w[1], w[2], w[3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(&P.g_out, stg, col0 + c0, row0, p);
+              bulk_commit();
+            }
+          }
+        }
+      } else {
+        const int rows = T.kind ? (int)P.m_pad : P.vn;
+        const bool f32 = T.kind || P.dt_f32;
+        const CUtensorMap* map = T.kind ? &P.dx_out : &P.dt_out;
+        const int out_row = T.kind ? row0 : P.dt_row0 + row0, plane = T.kind ? P.dx_plane0 + T.split : T.split;
+#pragma unroll
+        for (int c0 = 0; c0 < BN / 2; c0 += 32) {
+          if (row0 >= rows || col0 + c0 >= P.d) continue;
+          float own[FLUSH ? 1 : 32];
+          float* v = FLUSH ? sum + (FLUSH ? c0 : 0) : own;
+          if (!FLUSH) cols32(c0, v);
+          const int h = f32 ? 0 : (c0 >> 5) & 1;  // bf16: two groups of 32 columns fill a 128-byte row
+          if (h == 0) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+          }
+          if (f32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                           __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) w[q] = pack_bf16_rn(v[8 * j + 2 * q], v[8 * j + 2 * q + 1]);
+              st_shared_v4(stg_row + (((uint32_t)(4 * h + j) << 4) ^ swz), w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (f32 || h == 1 || col0 + c0 + 32 >= P.d) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_3d(map, stg, col0 + c0 - 32 * h, out_row, plane);
+              bulk_commit();
+            }
+          }
+        }
+      }
+      if (!FLUSH) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&accempty[(n - 1u) & 1u]);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// rows: which are live, gathered together
+// ---------------------------------------------------------------------------------------------
+struct Rows {
+  const int32_t* targets;  // cross entropy: a row is live when its target is in [0, vocab)
+  const uint8_t* flags;    // distillation: live flags of teacher_rows_kernel
+  int32_t vocab;
+  int32_t m;
+};
+__device__ __forceinline__ bool row_live(const Rows& R, int r) {
+  return R.targets ? (uint32_t)R.targets[r] < (uint32_t)R.vocab : R.flags[r] != 0;
+}
+
+constexpr int kScanThreads = 1024;
+
+// rowmap[i] = the i-th live row in order, *live = their number. One CTA: 4096 rows a turn, ballots
+// inside a warp and a scan over the 32 warps' counts.
+__global__ void __launch_bounds__(kScanThreads) live_rows_kernel(const Rows R, int32_t* __restrict__ rowmap,
+                                                                 int32_t* __restrict__ live) {
+  __shared__ int32_t count[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int base = 0, turn = 0;
+  for (int r0 = 0; r0 < R.m; r0 += 4 * kScanThreads, turn ^= 1) {
+    uint32_t mask[4];
+    int mine = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t r = (int64_t)r0 + warp * 128 + u * 32 + lane;
+      mask[u] = __ballot_sync(0xffffffffu, r < R.m && row_live(R, (int)r));
+      mine += __popc(mask[u]);
+    }
+    if (lane == 0) count[turn][warp] = mine;
+    __syncthreads();
+    int before = lane < warp ? count[turn][lane] : 0, all = count[turn][lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xffffffffu, before, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    int at = base + before;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (mask[u] >> lane & 1u) rowmap[at + __popc(mask[u] & ((1u << lane) - 1u))] = r0 + warp * 128 + u * 32 + lane;
+      at += __popc(mask[u]);
+    }
+    base += all;
+  }
+  if (threadIdx.x == 0) *live = base;
+}
+
+struct GatherArgs {
+  Rows R;
+  const int32_t* rowmap;
+  const int32_t* live;
+  const void* x;          // [m][d]
+  int32_t d;
+  int64_t m_pad;
+  __nv_bfloat16* xg;      // [planes][m_pad][d]
+  // backward, per live row (pad rows: 0): c = dloss / tau, lse, target
+  const float* dloss;     // [m] or nullptr
+  const float* lse_in;    // [m]
+  float inv_tau;
+  float* c;
+  float* lse;
+  int32_t* tgt;           // nullptr: no targets
+  // rows that are not live: zeros
+  void* dx;               // [m][d] in x's dtype, or nullptr
+  float* zero1;           // [m] or nullptr
+  float* zero2;
+};
+
+constexpr int kRowThreads = 256;
+
+// One warp per row i: copies live row rowmap[i] to place i (float32 rows as three planes), zeroes the
+// places up to the next multiple of 256 past the live rows, and zeroes the outputs of row i when it is
+// not live itself.
+template <mmf_dtype XT>
+__global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const int live = *a.live, nck = a.d >> 3;
+  const int planes = XT == MMF_F32 ? PLANES : 1;
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  if (i < live) {
+    const int64_t r = a.rowmap[i];
+    for (int c = lane; c < nck; c += 32) {
+      uint4* o = reinterpret_cast<uint4*>(a.xg + i * a.d) + c;
+      if (XT == MMF_BF16) {
+        *o = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + r * a.d)[c];
+      } else {
+        const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x) + r * a.d) + 2 * c;
+        const float4 u = s[0], w = s[1];
+        const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+        uint32_t p[PLANES][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float a0, a1, a2, b0, b1, b2;
+          split3(v[2 * q], a0, a1, a2);
+          split3(v[2 * q + 1], b0, b1, b2);
+          p[0][q] = pack_bf16_hi(a0, b0);
+          p[1][q] = pack_bf16_hi(a1, b1);
+          p[2][q] = pack_bf16_hi(a2, b2);
+        }
+#pragma unroll
+        for (int j = 0; j < PLANES; ++j)
+          *reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d + 8 * c) = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+      }
+    }
+    if (lane == 0 && a.c) {
+      a.c[i] = a.dloss[r] * a.inv_tau;
+      a.lse[i] = a.lse_in[r];
+    }
+    if (lane == 0 && a.tgt) a.tgt[i] = a.R.targets[r];
+  } else if (i < (((int64_t)live + 255) & ~(int64_t)255)) {
+    for (int j = 0; j < planes; ++j)
+      for (int c = lane; c < nck; c += 32) *(reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d) + c) = z;
+    if (lane == 0 && a.c) a.c[i] = a.lse[i] = 0.0f;
+    if (lane == 0 && a.tgt) a.tgt[i] = -1;
+  }
+  if (i < a.R.m && !row_live(a.R, (int)i)) {
+    if (a.dx) {
+      const int n16 = XT == MMF_F32 ? 2 * nck : nck;
+      uint4* o = reinterpret_cast<uint4*>(a.dx) + i * n16;
+      for (int c = lane; c < n16; c += 32) o[c] = z;
+    }
+    if (lane == 0 && a.zero1) a.zero1[i] = 0.0f;
+    if (lane == 0 && a.zero2) a.zero2[i] = 0.0f;
+  }
+}
+
+// float32 table -> three bf16 planes [3][count], 8 values a thread.
+__global__ void __launch_bounds__(kRowThreads) split_table_kernel(const float* __restrict__ t, int64_t count,
+                                                                  __nv_bfloat16* __restrict__ out) {
+  const int64_t n8 = count >> 3;
+  for (int64_t e = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; e < n8; e += (int64_t)gridDim.x * kRowThreads) {
+    const float4 u = reinterpret_cast<const float4*>(t)[2 * e], w = reinterpret_cast<const float4*>(t)[2 * e + 1];
+    const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+    uint32_t p[PLANES][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float a0, a1, a2, b0, b1, b2;
+      split3(v[2 * q], a0, a1, a2);
+      split3(v[2 * q + 1], b0, b1, b2);
+      p[0][q] = pack_bf16_hi(a0, b0);
+      p[1][q] = pack_bf16_hi(a1, b1);
+      p[2][q] = pack_bf16_hi(a2, b2);
+    }
+#pragma unroll
+    for (int j = 0; j < PLANES; ++j)
+      reinterpret_cast<uint4*>(out + j * count)[e] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// joining the tiles' statistics
+// ---------------------------------------------------------------------------------------------
+// lse_i = top / tau + log sum_j S_j exp((M_j - top) / tau) over the row's parts, and for the cross
+// entropy loss_i = lse_i - s_target / tau. CTA = 32 rows x 8 lanes over the parts.
+__global__ void __launch_bounds__(256) join_stats_kernel(const float2* __restrict__ part, int parts, int64_t m_pad,
+                                                         const int32_t* __restrict__ live_p,
+                                                         const int32_t* __restrict__ rowmap,
+                                                         const float* __restrict__ st, float inv_tau, float* loss,
+                                                         float* lse_out) {
+  __shared__ float2 red[8][32];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int live = *live_p;
+  const int64_t i = (int64_t)blockIdx.x * 32 + tx;
+  if ((int64_t)blockIdx.x * 32 >= live) return;
+  float mx = -INFINITY, sum = 0.0f;
+  if (i < live) {
+    for (int j = ty; j < parts; j += 8) {
+      const float2 p = part[(int64_t)j * m_pad + i];
+      const float top = fmaxf(mx, p.x);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      sum = sum * expf((mx - ref) * inv_tau) + p.y * expf((p.x - ref) * inv_tau);
+      mx = top;
+    }
+  }
+  red[ty][tx] = make_float2(mx, sum);
+  __syncthreads();
+  if (ty == 0 && i < live) {
+    float top = -INFINITY, s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, red[j][tx].x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += red[j][tx].y * expf((red[j][tx].x - ref) * inv_tau);
+    const float l = top * inv_tau + logf(s);
+    const int64_t r = rowmap[i];
+    lse_out[r] = l;
+    if (st) loss[r] = l - st[i] * inv_tau;
+  }
+}
+
+// out[row(i)][:] = sum over planes of part[p][i][:], in plane order; rows i < *count (or count_h),
+// written to rowmap[i] when given. 8 columns a thread.
+template <mmf_dtype OT>
+__global__ void __launch_bounds__(kRowThreads) join_planes_kernel(const float* __restrict__ part, int planes,
+                                                                  int64_t plane_rows, int d,
+                                                                  const int32_t* __restrict__ count_p, int64_t count_h,
+                                                                  const int32_t* __restrict__ rowmap, void* out) {
+  const int nck = d >> 3;
+  const int64_t rows = count_p ? *count_p : count_h;
+  const int64_t total = rows * nck;
+  for (int64_t e = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; e < total; e += (int64_t)gridDim.x * kRowThreads) {
+    const int64_t i = e / nck;
+    const int c = (int)(e - i * nck);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int p = 0; p < planes; ++p) {
+      const float4* s = reinterpret_cast<const float4*>(part + (p * plane_rows + i) * d) + 2 * c;
+      const float4 u = s[0], w = s[1];
+      v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+      v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
+    }
+    const int64_t r = rowmap ? rowmap[i] : i;
+    if (OT == MMF_F32) {
+      float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + r * d) + 2 * c;
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + r * d)[c] =
+          make_uint4(pack_bf16_rn(v[0], v[1]), pack_bf16_rn(v[2], v[3]), pack_bf16_rn(v[4], v[5]), pack_bf16_rn(v[6], v[7]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// the teacher's entries
+// ---------------------------------------------------------------------------------------------
+struct Teacher {
+  const int32_t* ids;   // [m][k]
+  const void* logits;   // [m][k]
+  mmf_dtype dt;
+  int32_t k;
+  int32_t vocab;
+  float inv_tau;
+};
+__device__ __forceinline__ bool teacher_valid(const Teacher& t, int64_t at, float& logit) {
+  logit = load_as_float(t.logits, at, t.dt);
+  return (uint32_t)t.ids[at] < (uint32_t)t.vocab && !(logit == -INFINITY);
+}
+
+// flags[r] = 1 when row r has a valid entry. One warp per row.
+__global__ void __launch_bounds__(kRowThreads) teacher_rows_kernel(const Teacher t, int64_t m, uint8_t* __restrict__ flags) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (r >= m) return;
+  bool any = false;
+  for (int j = lane; j < t.k; j += 32) {
+    float l;
+    any |= teacher_valid(t, r * t.k + j, l);
+  }
+  any = __any_sync(0xffffffffu, any);
+  if (lane == 0) flags[r] = any ? 1 : 0;
+}
+
+// The row's teacher distribution over its valid entries: top = the largest valid logit, total = sum
+// exp((t_j - top) / tau). Whole warp; the differences are taken before the division by tau, so that
+// logits near the type's lowest value stay finite.
+__device__ __forceinline__ void teacher_softmax(const Teacher& t, int64_t r, int lane, float& top, float& total) {
+  top = -INFINITY;
+  bool nan = false;
+  for (int j = lane; j < t.k; j += 32) {
+    float l;
+    if (teacher_valid(t, r * t.k + j, l)) {
+      nan |= l != l;
+      top = fmaxf(top, l);
+    }
+  }
+  top = warp_max(top);
+  if (__any_sync(0xffffffffu, nan)) top = __int_as_float(0x7fc00000);
+  total = 0.0f;
+  for (int j = lane; j < t.k; j += 32) {
+    float l;
+    if (teacher_valid(t, r * t.k + j, l)) total += expf((l - top) * t.inv_tau);
+  }
+  total = warp_sum(total);
+}
+
+constexpr int kDistillThreads = 256;
+
+// One CTA per row: s_j = x . T[id_j] for the valid entries (float32 accumulation, a warp per entry),
+// then loss = sum_j q_j (log q_j - s_j / tau + lse). Rows that are not live get zeros.
+template <mmf_dtype XT, mmf_dtype TT>
+__global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(const Teacher t, const uint8_t* __restrict__ flags,
+                                                                       const void* __restrict__ x,
+                                                                       const void* __restrict__ table, int d,
+                                                                       const float* __restrict__ lse, float* loss,
+                                                                       float* s_top) {
+  extern __shared__ __align__(16) float xs[];  // [d]
+  __shared__ float sj[MAX_TOP];
+  const int64_t r = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nck = d >> 3;
+  if (!flags[r]) {  // uniform across the CTA; loss and lse are zeroed by the gather
+    for (int j = threadIdx.x; j < t.k; j += kDistillThreads) s_top[r * t.k + j] = 0.0f;
+    return;
+  }
+  for (int c = threadIdx.x; c < d; c += kDistillThreads) xs[c] = load_as_float(x, r * d + c, XT);
+  __syncthreads();
+  for (int j = warp; j < t.k; j += kDistillThreads / 32) {
+    float l, acc = 0.0f;
+    const bool valid = teacher_valid(t, r * t.k + j, l);
+    if (valid) {
+      const int64_t row = (int64_t)t.ids[r * t.k + j] * d;
+      for (int c = lane; c < nck; c += 32) {
+        const float4 u = reinterpret_cast<const float4*>(xs)[2 * c], w = reinterpret_cast<const float4*>(xs)[2 * c + 1];
+        if (TT == MMF_F32) {
+          const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(table) + row) + 2 * c;
+          const float4 a = p[0], b = p[1];
+          acc = fmaf(a.x, u.x, acc); acc = fmaf(a.y, u.y, acc); acc = fmaf(a.z, u.z, acc); acc = fmaf(a.w, u.w, acc);
+          acc = fmaf(b.x, w.x, acc); acc = fmaf(b.y, w.y, acc); acc = fmaf(b.z, w.z, acc); acc = fmaf(b.w, w.w, acc);
+        } else {
+          const uint4 p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(table) + row)[c];
+          acc = fmaf(__uint_as_float(p.x << 16), u.x, acc); acc = fmaf(__uint_as_float(p.x & 0xffff0000u), u.y, acc);
+          acc = fmaf(__uint_as_float(p.y << 16), u.z, acc); acc = fmaf(__uint_as_float(p.y & 0xffff0000u), u.w, acc);
+          acc = fmaf(__uint_as_float(p.z << 16), w.x, acc); acc = fmaf(__uint_as_float(p.z & 0xffff0000u), w.y, acc);
+          acc = fmaf(__uint_as_float(p.w << 16), w.z, acc); acc = fmaf(__uint_as_float(p.w & 0xffff0000u), w.w, acc);
+        }
+      }
+      acc = warp_sum(acc);
+    }
+    if (lane == 0) {
+      sj[j] = acc;
+      s_top[r * t.k + j] = acc;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    float top, total, sum = 0.0f;
+    teacher_softmax(t, r, lane, top, total);
+    const float log_total = logf(total), L = lse[r];
+    for (int j = lane; j < t.k; j += 32) {
+      float l;
+      if (teacher_valid(t, r * t.k + j, l)) {
+        const float e = (l - top) * t.inv_tau, q = expf(e) / total;
+        // an entry whose q underflows adds nothing (0 log 0 = 0); NaN goes through
+        if (!(q == 0.0f)) sum += q * ((e - log_total) - (sj[j] * t.inv_tau - L));
+      }
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) loss[r] = sum;
+  }
+}
+
+// The teacher's share of g for the piece [v0, v0 + vn): for every valid entry of live row i with its
+// id in the piece, g[i][id] = c (exp(s_j / tau - lse) - sum of q over the row's entries with that id),
+// computed whole in float32 from the kept s_j and stored over the softmax part (so nothing is rounded
+// twice). One warp per row; entries with one id write one value.
+__global__ void __launch_bounds__(kRowThreads) teacher_grad_kernel(const Teacher t, const int32_t* __restrict__ live_p,
+                                                                   const int32_t* __restrict__ rowmap,
+                                                                   const float* __restrict__ s_top,
+                                                                   const float* __restrict__ c_p,
+                                                                   const float* __restrict__ lse_p, int v0, int vn,
+                                                                   __nv_bfloat16* g, int64_t m_pad, int64_t ldg,
+                                                                   int planes) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (i >= *live_p) return;
+  const int64_t r = rowmap[i];
+  float top, total;
+  teacher_softmax(t, r, lane, top, total);
+  const float c = c_p[i], L = lse_p[i];
+  for (int j0 = 0; j0 < t.k; j0 += 32) {
+    const int j = j0 + lane;
+    float l = 0.0f;
+    const bool mine = j < t.k && teacher_valid(t, r * t.k + j, l) && t.ids[r * t.k + j] >= v0 &&
+                      t.ids[r * t.k + j] < v0 + vn;
+    const int id = mine ? t.ids[r * t.k + j] : -1;
+    // every entry of the row passes by once, in order
+    float q = 0.0f;
+    for (int b0 = 0; b0 < t.k; b0 += 32) {
+      const int b = b0 + lane;
+      float lb = 0.0f, qb = 0.0f;
+      int idb = -2;
+      if (b < t.k && teacher_valid(t, r * t.k + b, lb)) {
+        idb = t.ids[r * t.k + b];
+        qb = expf((lb - top) * t.inv_tau) / total;
+      }
+      for (int o = 0; o < 32; ++o) {
+        const int ido = __shfl_sync(0xffffffffu, idb, o);
+        const float qo = __shfl_sync(0xffffffffu, qb, o);
+        if (ido == id) q += qo;
+      }
+    }
+    if (mine) {
+      const float v = c * (expf(s_top[r * t.k + j] * t.inv_tau - L) - q);
+      __nv_bfloat16* o = g + i * ldg + (id - v0);
+      if (planes == 1) {
+        *o = __float2bfloat16_rn(v);
+      } else {
+        float p0, p1, p2;
+        split3(v, p0, p1, p2);
+        o[0] = __float2bfloat16_rn(p0);
+        o[m_pad * ldg] = __float2bfloat16_rn(p1);
+        o[2 * m_pad * ldg] = __float2bfloat16_rn(p2);
+      }
+    }
+  }
+}
+
+}  // namespace hl
+}  // namespace mmf

@@ -21,7 +21,9 @@
 #include "gemm_skinny.cuh"
 #include "gemm_tc.cuh"
 #include "head.cuh"
+#include "head_loss.cuh"
 #include "hgrn2.cuh"
+#include "rmsnorm.cuh"
 #include "backward.cuh"
 #include "validate.cuh"
 #include "kernels.cuh"
@@ -112,6 +114,8 @@ unsigned long long current_ctx_id() {
   return id;
 }
 
+constexpr int kHeadLossMaxD = 32768;  // hidden sizes of the head losses (a row fits shared memory)
+
 template <mmf_dtype ZT, mmf_dtype HT>
 cudaError_t scan_tile_attrs() {
   cudaError_t e = cudaSuccess;
@@ -141,7 +145,22 @@ cudaError_t head_tc_attrs() {
   return cudaFuncSetAttribute(head::head_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               head::tc_smem_bytes(head::kTcRowsMax));
 }
-
+cudaError_t head_loss_attrs() {
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void* f, int smem) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  set((const void*)hl::head_loss_kernel<hl::kStats, true>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, false>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, true>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kProducts, false>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kProducts, true>, hl::SMEM_BYTES);
+  set((const void*)hl::distill_loss_kernel<MMF_F32, MMF_F32>, kHeadLossMaxD * 4);
+  set((const void*)hl::distill_loss_kernel<MMF_F32, MMF_BF16>, kHeadLossMaxD * 4);
+  set((const void*)hl::distill_loss_kernel<MMF_BF16, MMF_F32>, kHeadLossMaxD * 4);
+  set((const void*)hl::distill_loss_kernel<MMF_BF16, MMF_BF16>, kHeadLossMaxD * 4);
+  return e;
+}
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -192,6 +211,7 @@ mmf_status device_info(DevInfo** out) {
       MMF_CUDA((head_attrs<MMF_BF16, MMF_F32>()));
       MMF_CUDA((head_attrs<MMF_BF16, MMF_BF16>()));
       MMF_CUDA(head_tc_attrs());
+      MMF_CUDA(head_loss_attrs());
       MMF_CUDA(cudaFuncSetAttribute(gb::bf16_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, gb::SMEM_BYTES));
       MMF_CUDA(cudaFuncSetAttribute(drow::row_stage_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(3 * drow::kMaxK * sizeof(float))));
@@ -234,6 +254,21 @@ mmf_status encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base,
   cuuint32_t estr[2] = {1, 1};
   CUresult r = g_encode(map, dt, 2, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MMF_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return MMF_OK;
+}
+
+// [dim2][dim1][dim0] with dim0 contiguous; strides in bytes, 128-byte swizzle, boxes one plane deep.
+mmf_status encode_3d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t dim0, uint64_t dim1,
+                     uint64_t dim2, uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1) {
+  MMF_TRY(get_encoder());
+  cuuint64_t dims[3] = {dim0, dim1, dim2};
+  cuuint64_t strides[2] = {stride1, stride2};
+  cuuint32_t box[3] = {box0, box1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MMF_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return MMF_OK;
@@ -973,6 +1008,338 @@ mmf_status head_tc_pass(const void* x, mmf_dtype xdt, int nb, int d, const float
   return MMF_OK;
 }
 
+// ---------------------------------------------------------------------------------------------
+// losses over the tied head
+// ---------------------------------------------------------------------------------------------
+// Bytes of g (all planes) that one vocabulary piece of the backward aims at. Pieces of the size of m
+// make the two products' tiles equally long.
+constexpr size_t kLossPieceBytes = (size_t)512 << 20;
+constexpr int64_t kLossMinPiece = 4096;
+constexpr int kLossSplitTiles = 148;  // K splits are added until a product has about this many tiles
+constexpr int kLossSplitBlocks = 8;   // ... of at least this many 64-wide k-blocks
+
+struct LossPlan {
+  int64_t m_pad;
+  int32_t px, pt, pg;       // bf16 planes of x, the table and g
+  int32_t parts;            // statistics parts per row
+  int64_t piece, ldg;       // vocabulary columns per piece, row pitch of g
+  int32_t pieces, dx_split, dt_split;
+  int32_t* live;
+  int32_t* rowmap;
+  uint8_t* flags;
+  __nv_bfloat16* xg;
+  __nv_bfloat16* tp;        // table planes (float32 tables)
+  float2* part;
+  float* st;
+  int32_t* tgt;
+  float *c, *lse;
+  __nv_bfloat16* g;
+  float* dxp;
+  float* dtp;
+  size_t bytes;
+};
+
+LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bool backward, void* base) {
+  LossPlan L;
+  memset(&L, 0, sizeof(L));
+  uint8_t* p = reinterpret_cast<uint8_t*>(base);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* r = p ? p + off : nullptr;
+    off += align256(bytes);
+    return r;
+  };
+  L.m_pad = (m + 255) / 256 * 256;
+  L.px = xf32 ? hl::PLANES : 1;
+  L.pt = tf32 ? hl::PLANES : 1;
+  L.pg = xf32 || tf32 ? hl::PLANES : 1;
+  const size_t M = (size_t)L.m_pad;
+  L.live = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
+  L.rowmap = reinterpret_cast<int32_t*>(take(M * 4));
+  L.flags = take(M);
+  L.xg = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.px * M * d * 2));
+  if (tf32) L.tp = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pt * vocab * d * 2));
+  L.tgt = reinterpret_cast<int32_t*>(take(M * 4));
+  if (!backward) {
+    L.parts = 2 * hl::cdiv(vocab, hl::BN);
+    L.part = reinterpret_cast<float2*>(take((size_t)L.parts * M * sizeof(float2)));
+    L.st = reinterpret_cast<float*>(take(M * 4));
+    L.bytes = off;
+    return L;
+  }
+  L.c = reinterpret_cast<float*>(take(M * 4));
+  L.lse = reinterpret_cast<float*>(take(M * 4));
+  const int64_t v256 = ((int64_t)vocab + 255) / 256 * 256;
+  int64_t piece = (int64_t)(kLossPieceBytes / (std::max<size_t>(M, 256) * 2 * L.pg)) / 256 * 256;
+  piece = std::min(std::max(piece, kLossMinPiece), v256);
+  L.pieces = (int32_t)((vocab + piece - 1) / piece);
+  L.piece = (v256 / 256 + L.pieces - 1) / L.pieces * 256;  // even pieces
+  L.pieces = (int32_t)((vocab + L.piece - 1) / L.piece);
+  L.ldg = L.piece;
+  const auto splits = [](int64_t tiles, int64_t kb) {
+    const int64_t want = tiles > 0 ? (kLossSplitTiles + tiles - 1) / tiles : 1;
+    return (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, kb / kLossSplitBlocks, 64}));
+  };
+  const int64_t nt = hl::cdiv(d, hl::BN);
+  L.dx_split = splits(L.m_pad / hl::BM * nt, L.piece / hl::BK);
+  L.dt_split = splits(hl::cdiv(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
+  L.g = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pg * M * L.ldg * 2));
+  L.dxp = reinterpret_cast<float*>(take((size_t)L.pieces * L.dx_split * M * d * 4));
+  if (L.dt_split > 1) L.dtp = reinterpret_cast<float*>(take((size_t)L.dt_split * vocab * d * 4));
+  L.bytes = off;
+  return L;
+}
+
+// Plane pairs (i, j) with i + j <= order, smallest terms first.
+hl::Prods loss_prods(int pa, int pb, int order) {
+  hl::Prods P;
+  memset(&P, 0, sizeof(P));
+  for (int o = order; o >= 0; --o)
+    for (int i = std::min(o, pa - 1); i >= 0; --i) {
+      const int j = o - i;
+      if (j >= pb) continue;
+      P.a[P.n] = (uint8_t)i;
+      P.b[P.n] = (uint8_t)j;
+      ++P.n;
+    }
+  return P;
+}
+
+// What the four loss calls share: the operands and, for distillation, the teacher.
+struct LossArgs {
+  const void* x;
+  mmf_dtype xdt;
+  int64_t m;
+  int32_t d;
+  const void* table;
+  mmf_dtype tdt;
+  int32_t vocab;
+  const int32_t* targets;  // cross entropy
+  hl::Teacher teacher;     // distillation (ids != nullptr)
+  float tau;
+};
+
+mmf_status check_loss(const LossArgs& a, const char* name, bool distill, int32_t top_k) {
+  MMF_CHECK_ARG(a.m >= 0 && a.m <= (1 << 30), "%s: m = %lld outside [0, 2^30]", name, (long long)a.m);
+  MMF_CHECK_ARG(a.d > 0 && a.d % 8 == 0 && a.d <= kHeadLossMaxD, "%s: d = %d is not a multiple of 8 in [8, %d]", name,
+                a.d, kHeadLossMaxD);
+  MMF_CHECK_ARG(a.vocab > 0 && a.vocab <= (1 << 30), "%s: vocab = %d outside [1, 2^30]", name, a.vocab);
+  MMF_CHECK_ARG(valid_dtype(a.xdt) && valid_dtype(a.tdt), "%s: bad dtype", name);
+  if (distill) {
+    MMF_CHECK_ARG(valid_dtype(a.teacher.dt), "%s: bad dtype of the teacher's logits", name);
+    MMF_CHECK_ARG(top_k >= 1 && top_k <= hl::MAX_TOP, "%s: %d teacher entries a row, outside [1, %d]", name, top_k,
+                  hl::MAX_TOP);
+    MMF_CHECK_ARG(a.tau >= 1e-3f && a.tau <= 1e3f, "%s: temperature %g outside [1e-3, 1e3]", name, (double)a.tau);
+  }
+  return MMF_OK;
+}
+
+// The launches before the products: live rows, gathered rows, table planes. Fills the parts of P
+// that every product launch shares.
+mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, hl::Params& P, const DevInfo& di,
+                     cudaStream_t st, int* launches) {
+  const unsigned row_ctas = (unsigned)(L.m_pad / (hl::kRowThreads / 32));
+  hl::Rows R;
+  R.targets = a.targets;
+  R.flags = L.flags;
+  R.vocab = a.vocab;
+  R.m = (int32_t)a.m;
+  if (!a.targets) {
+    launch_k(hl::teacher_rows_kernel, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, a.teacher, a.m, L.flags);
+    ++*launches;
+  }
+  launch_k(hl::live_rows_kernel, dim3(1), dim3(hl::kScanThreads), 0, st, R, L.rowmap, L.live);
+  ga.R = R;
+  ga.rowmap = L.rowmap;
+  ga.live = L.live;
+  ga.x = a.x;
+  ga.d = a.d;
+  ga.m_pad = L.m_pad;
+  ga.xg = L.xg;
+  if (a.xdt == MMF_F32) launch_k(hl::gather_rows_kernel<MMF_F32>, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, ga);
+  else launch_k(hl::gather_rows_kernel<MMF_BF16>, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, ga);
+  *launches += 2;
+  const void* table = a.table;
+  if (a.tdt == MMF_F32) {
+    const int64_t count = (int64_t)a.vocab * a.d;
+    const unsigned ctas = (unsigned)std::min<int64_t>((count / 8 + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di.sms * 16);
+    launch_k(hl::split_table_kernel, dim3(ctas), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
+             count, L.tp);
+    ++*launches;
+    table = L.tp;
+  }
+  MMF_TRY(check_launch("head loss row kernels"));
+  const uint64_t row = (uint64_t)a.d * 2;
+  MMF_TRY(encode_3d(&P.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.xg, a.d, L.m_pad, L.px, row, L.m_pad * row, hl::BK, 64));
+  MMF_TRY(encode_3d(&P.t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, table, a.d, a.vocab, L.pt, row, a.vocab * row, hl::BK, 64));
+  P.live = L.live;
+  P.d = a.d;
+  P.vocab = a.vocab;
+  P.m_pad = L.m_pad;
+  P.scale = hl::kLog2e / a.tau;
+  P.fwd = loss_prods(L.px, L.pt, 2);
+  P.wait_limit_us = g_wait_limit.load();
+  return MMF_OK;
+}
+
+template <int MODE, bool FLUSH>
+void loss_launch(const hl::Params& P, const DevInfo& di, cudaStream_t st) {
+  launch_k(hl::head_loss_kernel<MODE, FLUSH>, dim3((unsigned)di.sms), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
+}
+
+mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top, void* ws, size_t ws_bytes,
+                        cudaStream_t st) {
+  const LossPlan L = loss_plan(a.m, a.d, a.vocab, a.xdt == MMF_F32, a.tdt == MMF_F32, false, ws);
+  MMF_TRY(check_ws(ws, ws_bytes, L.bytes));
+  DevInfo* di;
+  MMF_TRY(device_info(&di));
+  LaunchScope ls(MMF_KERNEL_OTHER, (double)a.m * a.d * dsize(a.xdt) + (double)a.vocab * a.d * dsize(a.tdt) + a.m * 12.0, st);
+  int launches = 0;
+  hl::Params P;
+  memset(&P, 0, sizeof(P));
+  hl::GatherArgs ga;
+  memset(&ga, 0, sizeof(ga));
+  ga.zero1 = loss;
+  ga.zero2 = lse;
+  ga.tgt = a.targets ? L.tgt : nullptr;
+  MMF_TRY(loss_rows(a, L, ga, P, *di, st, &launches));
+  P.vn = a.vocab;
+  P.part = L.part;
+  P.st = L.st;
+  P.tgt = ga.tgt;
+  loss_launch<hl::kStats, true>(P, *di, st);
+  launch_k(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(256), 0, st, (const float2*)L.part, L.parts,
+           L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
+           1.0f / a.tau, loss, lse);
+  launches += 2;
+  if (!a.targets) {
+    const size_t smem = (size_t)a.d * 4;
+    const dim3 grid((unsigned)a.m), block(hl::kDistillThreads);
+#define MMF_DISTILL(X_, T_)                                                                                      \
+  launch_k(hl::distill_loss_kernel<X_, T_>, grid, block, smem, st, a.teacher, (const uint8_t*)L.flags, a.x, a.table, \
+           a.d, (const float*)lse, loss, s_top)
+    if (a.xdt == MMF_F32 && a.tdt == MMF_F32) MMF_DISTILL(MMF_F32, MMF_F32);
+    else if (a.xdt == MMF_F32) MMF_DISTILL(MMF_F32, MMF_BF16);
+    else if (a.tdt == MMF_F32) MMF_DISTILL(MMF_BF16, MMF_F32);
+    else MMF_DISTILL(MMF_BF16, MMF_BF16);
+#undef MMF_DISTILL
+    ++launches;
+  }
+  g_launches.fetch_add(launches - 1);  // the timing scope counted one launch itself
+  return check_launch("head loss kernels");
+}
+
+mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top, const float* dloss, void* dx,
+                         void* dtable, void* ws, size_t ws_bytes, cudaStream_t st) {
+  const LossPlan L = loss_plan(a.m, a.d, a.vocab, a.xdt == MMF_F32, a.tdt == MMF_F32, true, ws);
+  MMF_TRY(check_ws(ws, ws_bytes, L.bytes));
+  DevInfo* di;
+  MMF_TRY(device_info(&di));
+  LaunchScope ls(MMF_KERNEL_OTHER, (double)a.m * a.d * dsize(a.xdt) * (dx ? 2.0 : 1.0) +
+                 (double)a.vocab * a.d * dsize(a.tdt) * (dtable ? 2.0 : 1.0) + a.m * 16.0, st);
+  int launches = 0;
+  hl::Params P;
+  memset(&P, 0, sizeof(P));
+  hl::GatherArgs ga;
+  memset(&ga, 0, sizeof(ga));
+  ga.dloss = dloss;
+  ga.lse_in = lse;
+  ga.inv_tau = 1.0f / a.tau;
+  ga.c = L.c;
+  ga.lse = L.lse;
+  ga.tgt = a.targets ? L.tgt : nullptr;
+  ga.dx = dx;
+  MMF_TRY(loss_rows(a, L, ga, P, *di, st, &launches));
+  P.tgt = ga.tgt;
+  P.lse = L.lse;
+  P.c = L.c;
+  P.dxp = loss_prods(L.pg, L.pt, L.pg == 1 ? 0 : a.xdt == MMF_F32 ? 2 : 1);
+  P.dtp = loss_prods(L.pg, L.px, L.pg == 1 ? 0 : a.tdt == MMF_F32 ? 2 : 1);
+  P.dx_split = dx ? L.dx_split : 0;
+  P.dt_split = dtable ? L.dt_split : 0;
+  const uint64_t f32row = (uint64_t)a.d * 4, trow = (uint64_t)a.d * dsize(a.tdt);
+  MMF_TRY(encode_3d(&P.dx_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, L.dxp, a.d, L.m_pad, (uint64_t)L.pieces * L.dx_split,
+                    f32row, L.m_pad * f32row, 32, 32));
+  P.dt_f32 = L.dt_split > 1 || a.tdt == MMF_F32;
+  if (dtable) {
+    if (L.dt_split > 1)
+      MMF_TRY(encode_3d(&P.dt_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, L.dtp, a.d, a.vocab, L.dt_split, f32row,
+                        a.vocab * f32row, 32, 32));
+    else if (a.tdt == MMF_F32)
+      MMF_TRY(encode_3d(&P.dt_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dtable, a.d, a.vocab, 1, trow, a.vocab * trow, 32, 32));
+    else
+      MMF_TRY(encode_3d(&P.dt_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dtable, a.d, a.vocab, 1, trow, a.vocab * trow, 64, 32));
+  }
+  for (int i = 0; i < L.pieces; ++i) {
+    P.v0 = (int32_t)(i * L.piece);
+    P.vn = (int32_t)std::min<int64_t>(L.piece, a.vocab - P.v0);
+    const uint64_t grow = (uint64_t)L.ldg * 2;
+    MMF_TRY(encode_3d(&P.g, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.g, P.vn, L.m_pad, L.pg, grow, L.m_pad * grow, hl::BK, 64));
+    MMF_TRY(encode_3d(&P.g_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.g, P.vn, L.m_pad, L.pg, grow, L.m_pad * grow, 64, 32));
+    P.dx_plane0 = i * L.dx_split;
+    P.dt_row0 = P.v0;
+    if (L.pg == 1) loss_launch<hl::kGrad, false>(P, *di, st);
+    else loss_launch<hl::kGrad, true>(P, *di, st);
+    if (!a.targets) {
+      launch_k(hl::teacher_grad_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
+               a.teacher, (const int32_t*)L.live, (const int32_t*)L.rowmap, s_top, (const float*)L.c,
+               (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.pg);
+      ++launches;
+    }
+    if (L.pg == 1) loss_launch<hl::kProducts, false>(P, *di, st);
+    else loss_launch<hl::kProducts, true>(P, *di, st);
+    launches += 2;
+  }
+  const auto join = [&](const float* part, int planes, int64_t rows, const int32_t* count, const int32_t* map,
+                        mmf_dtype odt, void* out) {
+    const unsigned ctas = (unsigned)std::min<int64_t>((rows * (a.d / 8) + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di->sms * 16);
+    if (odt == MMF_F32)
+      launch_k(hl::join_planes_kernel<MMF_F32>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
+    else
+      launch_k(hl::join_planes_kernel<MMF_BF16>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
+    ++launches;
+  };
+  if (dx) join(L.dxp, L.pieces * L.dx_split, L.m_pad, L.live, L.rowmap, a.xdt, dx);
+  if (dtable && L.dt_split > 1) join(L.dtp, L.dt_split, a.vocab, nullptr, nullptr, a.tdt, dtable);
+  g_launches.fetch_add(launches - 1);  // the timing scope counted one launch itself
+  return check_launch("head loss backward kernels");
+}
+
+// ---------------------------------------------------------------------------------------------
+// RMSNorm
+// ---------------------------------------------------------------------------------------------
+constexpr int kRmsMaxParts = 1024;  // partial rows of the gain's gradient (CTAs of the backward)
+
+// Rows per CTA turn, and the vector kernels' shape: threads x chunks cover d / 8.
+struct RmsPlan {
+  bool vec;
+  int threads, chunks;
+};
+RmsPlan rms_plan(int32_t d, std::initializer_list<const void*> ptrs) {
+  RmsPlan p;
+  const int nck = d / 8;
+  p.vec = d % 8 == 0 && nck <= rms::kMaxThreads * rms::kMaxChunks;
+  for (const void* q : ptrs) p.vec = p.vec && aligned16(q);
+  p.chunks = nck <= rms::kMaxThreads ? 1 : nck <= 2 * rms::kMaxThreads ? 2 : 4;
+  p.threads = std::max(32, ((nck + p.chunks - 1) / p.chunks + 31) / 32 * 32);
+  return p;
+}
+
+template <mmf_dtype XT, mmf_dtype YT>
+void rms_fwd_launch(const rms::Args& a, const RmsPlan& p, const DevInfo& di, cudaStream_t st) {
+  const auto grid = [&](int rows) { return dim3((unsigned)std::min<int64_t>((a.m + rows - 1) / rows, (int64_t)di.sms * 16)); };
+  if (p.chunks == 1) launch_k(rms::rms_fwd_kernel<XT, YT, 1, 2>, grid(2), dim3(p.threads), 0, st, a);
+  else if (p.chunks == 2) launch_k(rms::rms_fwd_kernel<XT, YT, 2, 1>, grid(1), dim3(p.threads), 0, st, a);
+  else launch_k(rms::rms_fwd_kernel<XT, YT, 4, 1>, grid(1), dim3(p.threads), 0, st, a);
+}
+template <mmf_dtype XT, mmf_dtype GT>
+void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t st) {
+  const dim3 grid((unsigned)ctas);
+  if (p.chunks == 1) launch_k(rms::rms_bwd_kernel<XT, GT, 1, 2>, grid, dim3(p.threads), 0, st, a);
+  else if (p.chunks == 2) launch_k(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
+  else launch_k(rms::rms_bwd_kernel<XT, GT, 4, 1>, grid, dim3(p.threads), 0, st, a);
+}
+
 }  // namespace
 
 // =============================================================================================
@@ -1053,6 +1420,12 @@ size_t mmf_workspace_bytes(mmf_op op, int64_t m, int32_t d, int32_t inner, int32
       return d > 0 ? scan_ws_bytes(m, d) : 0;
     case MMF_OP_HEAD:
       return inner > 0 ? head_ws_bytes(inner, d) : 0;
+    case MMF_OP_RMSNORM_BWD:
+      return align256((size_t)kRmsMaxParts * d * sizeof(float));
+    case MMF_OP_HEAD_LOSS:
+    case MMF_OP_HEAD_LOSS_BWD:
+      return d > 0 && inner > 0 ? loss_plan(m, d, inner, (n_layers & 1) != 0, (n_layers & 2) != 0,
+                                            op == MMF_OP_HEAD_LOSS_BWD, nullptr).bytes : 0;
     case MMF_OP_BITLINEAR_BWD:
       return d > 0 && inner > 0 ? lin_bwd_plan(m, d, inner).bytes : 0;
     case MMF_OP_DECODE:
@@ -1919,6 +2292,151 @@ mmf_status mmf_hgrn2_recurrence(const void* q, const void* f, const void* i, mmf
   }
 #undef MMF_HGRN2
   return check_launch("hgrn2_recurrent_kernel");
+}
+
+// ---------------------------------------------------------------------------------------------
+// RMSNorm and its gradients
+// ---------------------------------------------------------------------------------------------
+mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
+                           void* y, mmf_dtype y_dtype, mmf_stream_t stream) {
+  MMF_CHECK_ARG(m >= 0 && d > 0, "rmsnorm: bad sizes m=%lld d=%d", (long long)m, d);
+  MMF_CHECK_ARG(valid_dtype(x_dtype) && valid_dtype(y_dtype), "rmsnorm: bad dtype");
+  MMF_CHECK_ARG(eps >= 0.0f, "rmsnorm: negative eps");
+  if (m == 0) return MMF_OK;
+  MMF_CHECK_ARG(x && y, "rmsnorm: null pointer");
+  DevInfo* di;
+  MMF_TRY(device_info(&di));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  rms::Args a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.w = norm_w; a.out = y; a.xdt = x_dtype; a.odt = y_dtype; a.m = m; a.d = d; a.eps = eps;
+  LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (dsize(x_dtype) + dsize(y_dtype)), st);
+  const RmsPlan p = rms_plan(d, {x, y, norm_w});
+  if (!p.vec) {
+    launch_k(rms::rms_fwd_any_kernel, dim3((unsigned)std::min<int64_t>(m, (int64_t)di->sms * 8)), dim3(rms::kGenThreads), 0, st, a);
+  } else if (x_dtype == MMF_F32) {
+    if (y_dtype == MMF_F32) rms_fwd_launch<MMF_F32, MMF_F32>(a, p, *di, st);
+    else rms_fwd_launch<MMF_F32, MMF_BF16>(a, p, *di, st);
+  } else {
+    if (y_dtype == MMF_F32) rms_fwd_launch<MMF_BF16, MMF_F32>(a, p, *di, st);
+    else rms_fwd_launch<MMF_BF16, MMF_BF16>(a, p, *di, st);
+  }
+  return check_launch("rmsnorm kernel");
+}
+
+mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
+                                const void* dy, mmf_dtype dy_dtype, void* dx, float* dnorm_w, void* ws,
+                                size_t ws_bytes, mmf_stream_t stream) {
+  MMF_CHECK_ARG(m >= 0 && d > 0, "rmsnorm backward: bad sizes m=%lld d=%d", (long long)m, d);
+  MMF_CHECK_ARG(valid_dtype(x_dtype) && valid_dtype(dy_dtype), "rmsnorm backward: bad dtype");
+  MMF_CHECK_ARG(eps >= 0.0f, "rmsnorm backward: negative eps");
+  MMF_CHECK_ARG(m == 0 || (x && dy && dx), "rmsnorm backward: null pointer");
+  if (m == 0 && !dnorm_w) return MMF_OK;
+  if (m > 0 && dnorm_w) MMF_TRY(check_ws(ws, ws_bytes, mmf_workspace_bytes(MMF_OP_RMSNORM_BWD, m, d, 0, 0)));
+  DevInfo* di;
+  MMF_TRY(device_info(&di));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (m == 0) {  // an empty sum
+    MMF_CUDA(cudaMemsetAsync(dnorm_w, 0, (size_t)d * sizeof(float), st));
+    return MMF_OK;
+  }
+  rms::Args a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.dy = dy; a.w = norm_w; a.out = dx; a.part = dnorm_w ? reinterpret_cast<float*>(ws) : nullptr;
+  a.xdt = x_dtype; a.dydt = dy_dtype; a.odt = x_dtype; a.m = m; a.d = d; a.eps = eps;
+  LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (2.0 * dsize(x_dtype) + dsize(dy_dtype)), st);
+  const RmsPlan p = rms_plan(d, {x, dy, dx, norm_w});
+  const int rows = p.vec && p.chunks == 1 ? 2 : 1;
+  const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * 4, kRmsMaxParts});
+  if (!p.vec) {
+    launch_k(rms::rms_bwd_any_kernel, dim3((unsigned)ctas), dim3(rms::kGenThreads), 0, st, a);
+  } else if (x_dtype == MMF_F32) {
+    if (dy_dtype == MMF_F32) rms_bwd_launch<MMF_F32, MMF_F32>(a, p, ctas, st);
+    else rms_bwd_launch<MMF_F32, MMF_BF16>(a, p, ctas, st);
+  } else {
+    if (dy_dtype == MMF_F32) rms_bwd_launch<MMF_BF16, MMF_F32>(a, p, ctas, st);
+    else rms_bwd_launch<MMF_BF16, MMF_BF16>(a, p, ctas, st);
+  }
+  if (dnorm_w) {
+    launch_k(rms::rms_dw_kernel, dim3((unsigned)((d + 31) / 32)), dim3(1024), 0, st, (const float*)a.part, ctas, d, dnorm_w);
+    g_launches.fetch_add(1);  // two kernels under one timing scope
+  }
+  return check_launch("rmsnorm backward kernels");
+}
+
+// ---------------------------------------------------------------------------------------------
+// losses over the tied head
+// ---------------------------------------------------------------------------------------------
+mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, float* loss, float* lse,
+                                void* ws, size_t ws_bytes, mmf_stream_t stream) {
+  LossArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.xdt = x_dtype; a.m = m; a.d = d; a.table = table; a.tdt = table_dtype; a.vocab = vocab;
+  a.targets = targets; a.tau = 1.0f;
+  MMF_TRY(check_loss(a, "head xent", false, 0));
+  if (m == 0) return MMF_OK;
+  MMF_CHECK_ARG(x && table && targets && loss && lse, "head xent: null pointer");
+  MMF_CHECK_ARG(aligned16(x) && aligned16(table), "head xent: x / table not 16-byte aligned");
+  return loss_forward(a, loss, lse, nullptr, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// dtable of no rows
+mmf_status zero_dtable(void* dtable, int32_t vocab, int32_t d, mmf_dtype dt, mmf_stream_t stream) {
+  if (dtable) MMF_CUDA(cudaMemsetAsync(dtable, 0, (size_t)vocab * d * dsize(dt), reinterpret_cast<cudaStream_t>(stream)));
+  return MMF_OK;
+}
+
+mmf_status mmf_lm_head_xent_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                     mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, const float* lse,
+                                     const float* dloss, void* dx, void* dtable, void* ws, size_t ws_bytes,
+                                     mmf_stream_t stream) {
+  LossArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.xdt = x_dtype; a.m = m; a.d = d; a.table = table; a.tdt = table_dtype; a.vocab = vocab;
+  a.targets = targets; a.tau = 1.0f;
+  MMF_TRY(check_loss(a, "head xent backward", false, 0));
+  MMF_CHECK_ARG(aligned16(dx) && aligned16(dtable), "head xent backward: dx / dtable not 16-byte aligned");
+  if (m == 0) return zero_dtable(dtable, vocab, d, table_dtype, stream);
+  if (!dx && !dtable) return MMF_OK;
+  MMF_CHECK_ARG(x && table && targets && lse && dloss, "head xent backward: null pointer");
+  MMF_CHECK_ARG(aligned16(x) && aligned16(table), "head xent backward: x / table not 16-byte aligned");
+  return loss_backward(a, lse, nullptr, dloss, dx, dtable, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mmf_status mmf_lm_head_distill_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                   mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids, const void* t_logits,
+                                   mmf_dtype t_dtype, int32_t top_k, float temperature, float* loss, float* lse,
+                                   float* s_top, void* ws, size_t ws_bytes, mmf_stream_t stream) {
+  LossArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.xdt = x_dtype; a.m = m; a.d = d; a.table = table; a.tdt = table_dtype; a.vocab = vocab; a.tau = temperature;
+  a.teacher.ids = t_ids; a.teacher.logits = t_logits; a.teacher.dt = t_dtype; a.teacher.k = top_k;
+  a.teacher.vocab = vocab; a.teacher.inv_tau = 1.0f / temperature;
+  MMF_TRY(check_loss(a, "head distill", true, top_k));
+  if (m == 0) return MMF_OK;
+  MMF_CHECK_ARG(x && table && t_ids && t_logits && loss && lse && s_top, "head distill: null pointer");
+  MMF_CHECK_ARG(aligned16(x) && aligned16(table), "head distill: x / table not 16-byte aligned");
+  return loss_forward(a, loss, lse, s_top, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mmf_status mmf_lm_head_distill_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
+                                        mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids,
+                                        const void* t_logits, mmf_dtype t_dtype, int32_t top_k, float temperature,
+                                        const float* lse, const float* s_top, const float* dloss, void* dx,
+                                        void* dtable, void* ws, size_t ws_bytes, mmf_stream_t stream) {
+  LossArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = x; a.xdt = x_dtype; a.m = m; a.d = d; a.table = table; a.tdt = table_dtype; a.vocab = vocab; a.tau = temperature;
+  a.teacher.ids = t_ids; a.teacher.logits = t_logits; a.teacher.dt = t_dtype; a.teacher.k = top_k;
+  a.teacher.vocab = vocab; a.teacher.inv_tau = 1.0f / temperature;
+  MMF_TRY(check_loss(a, "head distill backward", true, top_k));
+  MMF_CHECK_ARG(aligned16(dx) && aligned16(dtable), "head distill backward: dx / dtable not 16-byte aligned");
+  if (m == 0) return zero_dtable(dtable, vocab, d, table_dtype, stream);
+  if (!dx && !dtable) return MMF_OK;
+  MMF_CHECK_ARG(x && table && t_ids && t_logits && lse && s_top && dloss, "head distill backward: null pointer");
+  MMF_CHECK_ARG(aligned16(x) && aligned16(table), "head distill backward: x / table not 16-byte aligned");
+  return loss_backward(a, lse, s_top, dloss, dx, dtable, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 mmf_status mmf_stack_fwd(const mmf_block_weights* layers, int32_t n_layers, const int32_t* ids,

@@ -1,0 +1,257 @@
+// rmsnorm.cuh -- K16: RMSNorm on its own (the model's final norm in training) and its gradients.
+//
+//   forward   rho = (mean(x^2) + eps)^(-1/2),  y = x rho w
+//   backward  u = dy w,  dx = rho u - rho^3 x mean(u x),  dw[c] = sum_r dy[r][c] x[r][c] rho_r
+//
+// Bound by HBM: one read of x (and dy), one write of y (dx). A CTA takes R rows at a time with every
+// thread holding the same 8-column chunks of each row in registers, so a row is read once, one block
+// reduction serves R rows, and in the backward the thread's share of dw stays in registers over all
+// rows of the CTA (written once as a partial row, added up in a fixed order by a second kernel).
+// Sums are float32; y, dx are rounded once to their type.
+#pragma once
+
+#include "common.cuh"
+
+namespace mmf {
+namespace rms {
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxChunks = 4;    // 8-column chunks per thread: rows of up to 16384
+constexpr int kGenThreads = 256;
+
+struct Args {
+  const void* x;        // [m][d]
+  const void* dy;       // backward [m][d]
+  const float* w;       // [d] or nullptr (1)
+  void* out;            // forward y, backward dx
+  float* part;          // backward [gridDim.x][d] partial dw, or nullptr
+  mmf_dtype xdt, dydt, odt;  // read by the general kernels
+  int64_t m;
+  int32_t d;
+  float eps;
+};
+
+template <mmf_dtype DT>
+__device__ __forceinline__ void load8(const void* p, int64_t idx, float (&v)[8]) {
+  if (DT == MMF_F32) {
+    const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + idx);
+    const float4 a = s[0], b = s[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + idx);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = __uint_as_float(u[q] << 16);
+      v[2 * q + 1] = __uint_as_float(u[q] & 0xffff0000u);
+    }
+  }
+}
+template <mmf_dtype DT>
+__device__ __forceinline__ void store8(void* p, int64_t idx, const float (&v)[8]) {
+  if (DT == MMF_F32) {
+    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + idx);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t u[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+      u[q] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p) + idx) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// Block sums of V values at once; red has V * 16 floats. One barrier before the result; the caller
+// alternates between two red arrays, so that the next call's writes cannot meet this call's reads.
+template <int V>
+__device__ __forceinline__ void block_sums(float (&v)[V], float (*red)[16]) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = warp_sum(v[i]);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) red[i][wid] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float s = 0.0f;
+    for (int w = 0; w < nw; ++w) s += red[i][w];
+    v[i] = s;
+  }
+}
+
+// d % 8 == 0, 16-byte aligned rows; chunk j of thread t is j * blockDim.x + t.
+template <mmf_dtype XT, mmf_dtype YT, int NC, int R>
+__global__ void __launch_bounds__(kMaxThreads) rms_fwd_kernel(const Args a) {
+  __shared__ float red[2][R][16];
+  const int nck = a.d >> 3, T = blockDim.x;
+  const float inv_d = 1.0f / (float)a.d;
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.m; r0 += (int64_t)gridDim.x * R, turn ^= 1) {
+    float x[R][NC][8], ss[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = j * T + (int)threadIdx.x;
+        if (r0 + r < a.m && c < nck) {
+          load8<XT>(a.x, (r0 + r) * a.d + 8 * c, x[r][j]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[r][j][e] = 0.0f;
+        }
+      }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      ss[r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss[r] = fmaf(x[r][j][e], x[r][j][e], ss[r]);
+    }
+    block_sums<R>(ss, red[turn]);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = j * T + (int)threadIdx.x;
+      if (c >= nck) continue;
+      float w[8] = {1, 1, 1, 1, 1, 1, 1, 1};
+      if (a.w) load8<MMF_F32>(a.w, 8 * c, w);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (r0 + r >= a.m) continue;
+        const float rho = rsqrtf(ss[r] * inv_d + a.eps);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[r][j][e] * rho * w[e];
+        store8<YT>(a.out, (r0 + r) * a.d + 8 * c, y);
+      }
+    }
+  }
+}
+
+template <mmf_dtype XT, mmf_dtype GT, int NC, int R>
+__global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
+  __shared__ float red[2][2 * R][16];
+  const int nck = a.d >> 3, T = blockDim.x;
+  const float inv_d = 1.0f / (float)a.d;
+  float w[NC][8], dw[NC][8];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    const int c = j * T + (int)threadIdx.x;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { w[j][e] = 1.0f; dw[j][e] = 0.0f; }
+    if (a.w && c < nck) load8<MMF_F32>(a.w, 8 * c, w[j]);
+  }
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.m; r0 += (int64_t)gridDim.x * R, turn ^= 1) {
+    float x[R][NC][8], g[R][NC][8], s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = j * T + (int)threadIdx.x;
+        if (r0 + r < a.m && c < nck) {
+          load8<XT>(a.x, (r0 + r) * a.d + 8 * c, x[r][j]);
+          load8<GT>(a.dy, (r0 + r) * a.d + 8 * c, g[r][j]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[r][j][e] = g[r][j][e] = 0.0f;
+        }
+      }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = s[R + r] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s[r] = fmaf(x[r][j][e], x[r][j][e], s[r]);
+          s[R + r] = fmaf(g[r][j][e] * w[j][e], x[r][j][e], s[R + r]);
+        }
+    }
+    block_sums<2 * R>(s, red[turn]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r0 + r >= a.m) continue;
+      const float rho = rsqrtf(s[r] * inv_d + a.eps);
+      const float k = rho * rho * rho * (s[R + r] * inv_d);
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = j * T + (int)threadIdx.x;
+        if (c >= nck) continue;
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[j][e] = fmaf(g[r][j][e] * rho, x[r][j][e], dw[j][e]);
+          o[e] = rho * (g[r][j][e] * w[j][e]) - k * x[r][j][e];
+        }
+        store8<XT>(a.out, (r0 + r) * a.d + 8 * c, o);
+      }
+    }
+  }
+  if (a.part) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = j * T + (int)threadIdx.x;
+      if (c < nck) store8<MMF_F32>(a.part, (int64_t)blockIdx.x * a.d + 8 * c, dw[j]);
+    }
+  }
+}
+
+// Any width and alignment: a CTA walks its rows one at a time, elements through memory twice.
+__global__ void __launch_bounds__(kGenThreads) rms_fwd_any_kernel(const Args a) {
+  __shared__ float red[32];
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
+    float ss = 0.0f;
+    for (int c = threadIdx.x; c < a.d; c += kGenThreads) {
+      const float v = load_as_float(a.x, r * a.d + c, a.xdt);
+      ss = fmaf(v, v, ss);
+    }
+    const float rho = rsqrtf(block_sum(ss, red) / (float)a.d + a.eps);
+    for (int c = threadIdx.x; c < a.d; c += kGenThreads)
+      store_from_float(a.out, r * a.d + c, a.odt, load_as_float(a.x, r * a.d + c, a.xdt) * rho * (a.w ? a.w[c] : 1.0f));
+  }
+}
+__global__ void __launch_bounds__(kGenThreads) rms_bwd_any_kernel(const Args a) {
+  __shared__ float red[32];
+  float* part = a.part ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
+  if (part)
+    for (int c = threadIdx.x; c < a.d; c += kGenThreads) part[c] = 0.0f;  // each thread only touches its own columns
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
+    float ss = 0.0f, ux = 0.0f;
+    for (int c = threadIdx.x; c < a.d; c += kGenThreads) {
+      const float v = load_as_float(a.x, r * a.d + c, a.xdt);
+      const float u = load_as_float(a.dy, r * a.d + c, a.dydt) * (a.w ? a.w[c] : 1.0f);
+      ss = fmaf(v, v, ss);
+      ux = fmaf(u, v, ux);
+    }
+    const float rho = rsqrtf(block_sum(ss, red) / (float)a.d + a.eps);
+    const float k = rho * rho * rho * (block_sum(ux, red) / (float)a.d);
+    for (int c = threadIdx.x; c < a.d; c += kGenThreads) {
+      const float v = load_as_float(a.x, r * a.d + c, a.xdt), g = load_as_float(a.dy, r * a.d + c, a.dydt);
+      if (part) part[c] = fmaf(g * rho, v, part[c]);
+      store_from_float(a.out, r * a.d + c, a.odt, rho * (g * (a.w ? a.w[c] : 1.0f)) - k * v);
+    }
+  }
+}
+
+// dw[c] = sum over the partial rows, in a fixed order: 32 columns x 32 lanes per CTA.
+__global__ void __launch_bounds__(1024) rms_dw_kernel(const float* __restrict__ part, int rows, int d, float* __restrict__ dw) {
+  __shared__ float red[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  float s = 0.0f;
+  if (c < d)
+    for (int r = ty; r < rows; r += 32) s += part[(int64_t)r * d + c];
+  red[ty][tx] = s;
+  __syncthreads();
+  const float v = warp_sum(red[tx][ty]);
+  if (tx == 0 && blockIdx.x * 32 + ty < d) dw[blockIdx.x * 32 + ty] = v;
+}
+
+}  // namespace rms
+}  // namespace mmf
