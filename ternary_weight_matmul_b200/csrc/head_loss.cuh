@@ -11,9 +11,12 @@
 // them together, and every kernel reads the live count on the device (no host synchronisation, and
 // what a dropped row holds, NaN included, reaches nothing).
 //
-// All three products are one warp-specialised tcgen05 kernel: a TMA producer thread, an MMA thread,
-// eight epilogue warps, persistent over tiles, two accumulators in tensor memory so that a tile's
-// epilogue runs under the next tile's MMAs. Operands are bf16; a float32 operand enters as three
+// All three products are one warp-specialised tcgen05 kernel on pairs of CTAs (cta_group::2): a pair
+// owns a 256 x 256 tile, each CTA loads its 128 rows of A and its 128 columns' half of B and holds its
+// 128 x 256 of D, so that a k-block costs 32 KB of L2 reads per CTA; with single CTAs and 128 x 256
+// tiles it is 48 KB, and those reads (13.5 TB/s) held the kernel at 1150 TFLOP/s. Per CTA a TMA
+// producer thread and eight epilogue warps, one MMA thread in the pair's first CTA, persistent over
+// tiles, two accumulators in tensor memory so that a tile's epilogue runs under the next tile's MMAs. Operands are bf16; a float32 operand enters as three
 // bf16 planes that add up to it exactly (8 + 8 + 8 significant bits, by truncation), and a product
 // of float32 accuracy runs over the plane pairs (i, j) with i + j <= 2, smallest terms first.
 //
@@ -29,14 +32,15 @@
 namespace mmf {
 namespace hl {
 
-constexpr int BM = 128;        // rows of D per tile (MMA M)
+constexpr int CM = 128;        // rows of D per CTA
+constexpr int BM = 2 * CM;     // rows of D per tile (MMA M, over the pair)
 constexpr int BN = 256;        // columns of D per tile (MMA N)
 constexpr int BK = 64;         // bf16 per k-block: one 128-byte swizzle atom
 constexpr int UK = 16;         // K per kind::f16 instruction
-constexpr int STAGES = 4;
-constexpr int FLUSH_KB = 4;    // k-blocks per accumulator where pieces are added in registers
+constexpr int STAGES = 6;
+constexpr int FLUSH_KB = 8;    // k-blocks per accumulator where pieces are added in registers
 constexpr int BOX_BYTES = 64 * BK * 2;  // every TMA load box: 64 x 64 bf16, 8 KB
-constexpr int A_BOXES = BM / 64, B_BOXES = BN / 64;
+constexpr int A_BOXES = CM / 64, B_BOXES = BN / 2 / 64;  // per CTA
 constexpr int STAGE_BYTES = (A_BOXES + B_BOXES) * BOX_BYTES;
 constexpr int EPI_WARPS = 8;   // two per tensor-memory lane quarter, each half of the columns
 constexpr int THREADS = (4 + EPI_WARPS) * 32;
@@ -87,12 +91,14 @@ struct Params {
 // ---------------------------------------------------------------------------------------------
 // PTX used here only
 // ---------------------------------------------------------------------------------------------
+// Load into this CTA's shared memory, counted on a barrier of either CTA of the pair (a
+// shared::cluster address).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
-                                            uint64_t* bar) {
+                                            uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
@@ -107,6 +113,48 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of `bar` in the pair's first CTA
+__device__ __forceinline__ uint32_t in_first_cta(const uint64_t* bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on `bar` (the same place in both CTAs) when all MMAs issued so far have completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 // 2^v by the hardware approximation (2 ulp over the range the softmax needs; 0 for -inf).
 __device__ __forceinline__ float ex2(float v) {
@@ -171,9 +219,9 @@ __device__ __forceinline__ Tile tile_at(const Params& P, int live, int t) {
   T.kind = 0;
   T.split = 0;
   if (MODE != kProducts) {
-    // groups of row tiles, columns slow inside a group: the CTAs of one wave share a few row tiles
+    // groups of row tiles, columns slow inside a group: the pairs of one wave share a few row tiles
     // and a few table tiles, which the L2 then serves
-    constexpr int G = 16;
+    constexpr int G = 8;
     const int mt = cdiv(live, BM), nt = cdiv(P.vn, BN);
     const int grp = t / (G * nt), rem = t - grp * (G * nt);
     const int gm = mt - grp * G < G ? mt - grp * G : G;
@@ -222,20 +270,24 @@ __device__ __forceinline__ int tile_segments(const Tile& T) {
 }
 
 template <int MODE, bool FLUSH>
-__global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_constant__ Params P) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_constant__ Params P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + STAGES * STAGE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI_WARPS * OUT_BYTES);
-  uint64_t* full = bars;                     // TMA -> MMA           (count 1 + tx bytes)
+  // full and accempty count in the pair's first CTA (both CTAs' copies and epilogue warps); empty,
+  // accfull and drain are each CTA's own, reached by the MMA thread's multicast commits
+  uint64_t* full = bars;                     // TMA -> MMA           (count 1 + both CTAs' bytes)
   uint64_t* empty = bars + STAGES;           // MMA commit -> TMA    (count 1)
   uint64_t* accfull = bars + 2 * STAGES;     // MMA commit -> epilogue, two accumulators
-  uint64_t* accempty = accfull + 2;          // epilogue -> MMA      (count EPI_WARPS)
-  uint64_t* drain = accempty + 2;            // MMA drain after an abort
+  uint64_t* accempty = accfull + 2;          // epilogues -> MMA     (count 2 * EPI_WARPS)
+  uint64_t* drain = accempty + 2;            // everything the MMA thread issued
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t limit = P.wait_limit_us;
+  const uint32_t rank = cluster_rank();
+  const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);  // this pair's tiles
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -244,15 +296,16 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&accfull[b], 1);
-      mbar_init(&accempty[b], EPI_WARPS);
+      mbar_init(&accempty[b], 2 * EPI_WARPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == 2) tmem_alloc(tmem_slot, TMEM_COLS);
+  if (warp == 2) tmem_alloc_pair(tmem_slot, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers and tensor memory are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int live = *P.live;
@@ -262,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (int t = first; ok && t < tiles; t += stride) {
         const Tile T = tile_at<MODE>(P, live, t);
         const Prods& pr = MODE != kProducts ? P.fwd : T.kind ? P.dxp : P.dtp;
         for (int p = 0; ok && p < T.nprod; ++p) {
@@ -272,30 +325,38 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
             if (!mbar_wait_bounded(&empty[s], ph ^ 1u, limit, abort_flag)) { ok = false; break; }
             const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BOXES * BOX_BYTES;
             const int k = (T.kb0 + kb) * BK;
-            mbar_arrive_expect_tx(&full[s], STAGE_BYTES);
+            const uint32_t bar = in_first_cta(&full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
+            const int arow = T.row + CM * (int)rank, bcol = T.col + BN / 2 * (int)rank;
             if (MODE != kProducts) {
 #pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, T.row + 64 * i, pa, &full[s]);
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, arow + 64 * i, pa, bar);
 #pragma unroll
               for (int i = 0; i < B_BOXES; ++i)
-                tma_load_3d(sb + i * BOX_BYTES, &P.t, k, P.v0 + T.col + 64 * i, pb, &full[s]);
+                tma_load_3d(sb + i * BOX_BYTES, &P.t, k, P.v0 + bcol + 64 * i, pb, bar);
             } else if (T.kind == 0) {  // dT = g^T x: both operands MN-major, k = live rows
 #pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, T.row + 64 * i, k, pa, &full[s]);
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, arow + 64 * i, k, pa, bar);
 #pragma unroll
-              for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.x, T.col + 64 * i, k, pb, &full[s]);
+              for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.x, bcol + 64 * i, k, pb, bar);
             } else {  // dx = g T: A K-major, B MN-major, k = vocabulary
 #pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, k, T.row + 64 * i, pa, &full[s]);
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, k, arow + 64 * i, pa, bar);
 #pragma unroll
               for (int i = 0; i < B_BOXES; ++i)
-                tma_load_3d(sb + i * BOX_BYTES, &P.t, T.col + 64 * i, P.v0 + k, pb, &full[s]);
+                tma_load_3d(sb + i * BOX_BYTES, &P.t, bcol + 64 * i, P.v0 + k, pb, bar);
             }
           }
         }
       }
-      if (!ok) {
-        // drain: the stages armed in the last STAGES iterations must see their copies land
+      if (ok) {
+        // the last stages' commits have reached this CTA before it ends
+        for (uint32_t j = it > STAGES ? it - STAGES : 0; ok && j < it; ++j)
+          ok = mbar_wait_bounded(&empty[j % STAGES], (j / STAGES) & 1u, limit, abort_flag);
+      }
+      if (!ok && rank == 0) {
+        // drain: the stages armed in the last STAGES iterations must see their copies land (the other
+        // CTA's among them; it cannot end before this one)
         for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
           mbar_wait_drain(&full[j % STAGES], (j / STAGES) & 1u);
       }
@@ -303,14 +364,14 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       // kind::f16: D float32 (bits 4-5 = 1), A and B bf16 (bits 7-9, 10-12 = 1), MN-major A / B at
       // bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28
       constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
                                   ((uint32_t)(BM >> 4) << 24);
       uint32_t it = 0, n = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      for (int t = first; ok && t < tiles; t += stride) {
         const Tile T = tile_at<MODE>(P, live, t);
         const bool a_mn = MODE == kProducts && T.kind == 0, b_mn = MODE == kProducts;
         const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
@@ -329,15 +390,15 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
             for (int kk = 0; kk < BK / UK; ++kk) {
               const uint64_t ad = a_mn ? mn128_desc(sa + kk * UK * 128) : sw128_desc(sa + kk * UK * 2);
               const uint64_t bd = b_mn ? mn128_desc(sb + kk * UK * 128) : sw128_desc(sb + kk * UK * 2);
-              tc_mma_bf16_ss(acc, ad, bd, idesc, (i | kk) != 0 ? 1u : 0u);
+              tc_mma_bf16_pair(acc, ad, bd, idesc, (i | kk) != 0 ? 1u : 0u);
             }
-            tc_commit(&empty[s]);
+            tc_commit_pair(&empty[s]);
           }
-          if (ok) tc_commit(&accfull[buf]);
+          if (ok) tc_commit_pair(&accfull[buf]);
         }
       }
       // everything issued has completed before this thread reaches the teardown barrier
-      tc_commit(drain);
+      tc_commit_pair(drain);
       mbar_wait_drain(drain, 0u);
     }
     __syncwarp();
@@ -348,9 +409,9 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
     const uint32_t swz = (uint32_t)(lane & 7) << 4, stg_row = stg + lane * 128;
     uint32_t n = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+    for (int t = first; ok && t < tiles; t += stride) {
       const Tile T = tile_at<MODE>(P, live, t);
-      const int row0 = T.row + quarter * 32, row = row0 + lane;
+      const int row0 = T.row + CM * (int)rank + quarter * 32, row = row0 + lane;
       const int col0 = T.col + half * (BN / 2);
       const bool zero = T.nprod * T.nkb == 0;  // no k-blocks: the accumulator was never written
       uint32_t acc = 0;
@@ -375,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&accempty[buf]);
+          if (lane == 0) mbar_arrive_cluster(in_first_cta(&accempty[buf]));
         }
       }
       if (!ok) break;
@@ -510,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
       if (!FLUSH) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&accempty[(n - 1u) & 1u]);
+        if (lane == 0) mbar_arrive_cluster(in_first_cta(&accempty[(n - 1u) & 1u]));
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -518,9 +579,13 @@ __global__ void __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_cons
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA ends, or frees tensor memory, while the other one's MMAs, copies or arrivals can reach it
+  if (rank == 1 && threadIdx.x == 0) mbar_wait_drain(drain, 0u);
+  __syncthreads();
+  cluster_sync();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc_pair(tmem, TMEM_COLS);
   }
 }
 

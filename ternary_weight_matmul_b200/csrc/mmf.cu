@@ -1015,7 +1015,7 @@ mmf_status head_tc_pass(const void* x, mmf_dtype xdt, int nb, int d, const float
 // make the two products' tiles equally long.
 constexpr size_t kLossPieceBytes = (size_t)512 << 20;
 constexpr int64_t kLossMinPiece = 4096;
-constexpr int kLossSplitTiles = 148;  // K splits are added until a product has about this many tiles
+constexpr int kLossSplitTiles = 74;   // K splits are added until a product has about this many tiles
 constexpr int kLossSplitBlocks = 8;   // ... of at least this many 64-wide k-blocks
 
 struct LossPlan {
@@ -1184,7 +1184,7 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, hl
 
 template <int MODE, bool FLUSH>
 void loss_launch(const hl::Params& P, const DevInfo& di, cudaStream_t st) {
-  launch_k(hl::head_loss_kernel<MODE, FLUSH>, dim3((unsigned)di.sms), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
+  launch_k(hl::head_loss_kernel<MODE, FLUSH>, dim3((unsigned)di.sms & ~1u), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
 }
 
 mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top, void* ws, size_t ws_bytes,
