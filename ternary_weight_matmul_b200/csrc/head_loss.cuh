@@ -303,6 +303,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
     mbar_fence_init();
   }
   if (warp == 2) tmem_alloc_pair(tmem_slot, TMEM_COLS);
+  if (warp == 3 && lane == 0) {
+    tma_prefetch_desc(&P.x);
+    tma_prefetch_desc(&P.t);
+    if (MODE == kProducts) tma_prefetch_desc(&P.g);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers and tensor memory are set up
@@ -662,61 +667,116 @@ struct GatherArgs {
 
 constexpr int kRowThreads = 256;
 
-// One warp per row i: copies live row rowmap[i] to place i (float32 rows as three planes), zeroes the
-// places up to the next multiple of 256 past the live rows, and zeroes the outputs of row i when it is
-// not live itself.
+// Live row r -> place i (float32 rows as three planes). Whole warp, as the next two.
+template <mmf_dtype XT>
+__device__ __forceinline__ void place_row(const GatherArgs& a, int64_t i, int64_t r, int lane) {
+  const int nck = a.d >> 3;
+  for (int c = lane; c < nck; c += 32) {
+    if (XT == MMF_BF16) {
+      reinterpret_cast<uint4*>(a.xg + i * a.d)[c] =
+          reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + r * a.d)[c];
+    } else {
+      const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x) + r * a.d) + 2 * c;
+      const float4 u = s[0], w = s[1];
+      const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+      uint32_t p[PLANES][4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float a0, a1, a2, b0, b1, b2;
+        split3(v[2 * q], a0, a1, a2);
+        split3(v[2 * q + 1], b0, b1, b2);
+        p[0][q] = pack_bf16_hi(a0, b0);
+        p[1][q] = pack_bf16_hi(a1, b1);
+        p[2][q] = pack_bf16_hi(a2, b2);
+      }
+#pragma unroll
+      for (int j = 0; j < PLANES; ++j)
+        reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d)[c] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+    }
+  }
+  if (lane == 0 && a.c) {
+    a.c[i] = a.dloss[r] * a.inv_tau;
+    a.lse[i] = a.lse_in[r];
+  }
+  if (lane == 0 && a.tgt) a.tgt[i] = a.R.targets[r];
+}
+// zeros in a place past the live rows
+template <mmf_dtype XT>
+__device__ __forceinline__ void zero_place(const GatherArgs& a, int64_t i, int lane) {
+  for (int j = 0; j < (XT == MMF_F32 ? PLANES : 1); ++j)
+    for (int c = lane; c < a.d >> 3; c += 32)
+      reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d)[c] = make_uint4(0u, 0u, 0u, 0u);
+  if (lane == 0 && a.c) a.c[i] = a.lse[i] = 0.0f;
+  if (lane == 0 && a.tgt) a.tgt[i] = -1;
+}
+// zeros in the outputs of a row that is not live
+template <mmf_dtype XT>
+__device__ __forceinline__ void zero_outputs(const GatherArgs& a, int64_t r, int lane) {
+  if (a.dx) {
+    const int n16 = (a.d >> 3) * (XT == MMF_F32 ? 2 : 1);
+    for (int c = lane; c < n16; c += 32) reinterpret_cast<uint4*>(a.dx)[r * n16 + c] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (lane == 0 && a.zero1) a.zero1[r] = 0.0f;
+  if (lane == 0 && a.zero2) a.zero2[r] = 0.0f;
+}
+
+// One warp per row i: fills place i from live row rowmap[i], or with zeros up to the next multiple of
+// 256 past the live rows, and zeroes the outputs of row i when it is not live itself.
 template <mmf_dtype XT>
 __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int live = *a.live, nck = a.d >> 3;
-  const int planes = XT == MMF_F32 ? PLANES : 1;
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  if (i < live) {
-    const int64_t r = a.rowmap[i];
-    for (int c = lane; c < nck; c += 32) {
-      uint4* o = reinterpret_cast<uint4*>(a.xg + i * a.d) + c;
-      if (XT == MMF_BF16) {
-        *o = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + r * a.d)[c];
-      } else {
-        const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x) + r * a.d) + 2 * c;
-        const float4 u = s[0], w = s[1];
-        const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-        uint32_t p[PLANES][4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float a0, a1, a2, b0, b1, b2;
-          split3(v[2 * q], a0, a1, a2);
-          split3(v[2 * q + 1], b0, b1, b2);
-          p[0][q] = pack_bf16_hi(a0, b0);
-          p[1][q] = pack_bf16_hi(a1, b1);
-          p[2][q] = pack_bf16_hi(a2, b2);
-        }
-#pragma unroll
-        for (int j = 0; j < PLANES; ++j)
-          *reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d + 8 * c) = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
-      }
-    }
-    if (lane == 0 && a.c) {
-      a.c[i] = a.dloss[r] * a.inv_tau;
-      a.lse[i] = a.lse_in[r];
-    }
-    if (lane == 0 && a.tgt) a.tgt[i] = a.R.targets[r];
-  } else if (i < (((int64_t)live + 255) & ~(int64_t)255)) {
-    for (int j = 0; j < planes; ++j)
-      for (int c = lane; c < nck; c += 32) *(reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d) + c) = z;
-    if (lane == 0 && a.c) a.c[i] = a.lse[i] = 0.0f;
-    if (lane == 0 && a.tgt) a.tgt[i] = -1;
+  const int live = *a.live;
+  if (i < live) place_row<XT>(a, i, a.rowmap[i], lane);
+  else if (i < (((int64_t)live + 255) & ~(int64_t)255)) zero_place<XT>(a, i, lane);
+  if (i < a.R.m && !row_live(a.R, (int)i)) zero_outputs<XT>(a, i, lane);
+}
+
+// live_rows_kernel and gather_rows_kernel in one launch, for few rows: every CTA counts the live rows
+// before its own eight (m / 256 flags a thread, out of the L2), a live row goes to the place that gives
+// it, and the rows that are not live and those past m fill the places behind with zeros. Below
+// kOneLaunchRows this is 2.5 us less than the two launches; the counting grows with m^2.
+constexpr int kOneLaunchRows = 4096;
+template <mmf_dtype XT>
+__global__ void __launch_bounds__(kRowThreads) place_rows_kernel(const GatherArgs a, int32_t* __restrict__ rowmap,
+                                                                 int32_t* __restrict__ live_out) {
+  __shared__ int32_t counts[2][kRowThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r0 = blockIdx.x * (kRowThreads / 32);
+  int before = 0, total = 0;
+  for (int r = threadIdx.x; r < a.R.m; r += kRowThreads) {
+    const int is = row_live(a.R, r) ? 1 : 0;
+    total += is;
+    if (r < r0) before += is;
   }
-  if (i < a.R.m && !row_live(a.R, (int)i)) {
-    if (a.dx) {
-      const int n16 = XT == MMF_F32 ? 2 * nck : nck;
-      uint4* o = reinterpret_cast<uint4*>(a.dx) + i * n16;
-      for (int c = lane; c < n16; c += 32) o[c] = z;
-    }
-    if (lane == 0 && a.zero1) a.zero1[i] = 0.0f;
-    if (lane == 0 && a.zero2) a.zero2[i] = 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
   }
+  if (lane == 0) {
+    counts[0][warp] = before;
+    counts[1][warp] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) {
+    before += counts[0][w];
+    total += counts[1][w];
+  }
+  const uint32_t mine = __ballot_sync(0xffffffffu, lane < kRowThreads / 32 && r0 + lane < a.R.m && row_live(a.R, r0 + lane));
+  const int64_t r = r0 + warp;
+  before += __popc(mine & ((1u << warp) - 1u));
+  if (mine >> warp & 1u) {
+    if (lane == 0) rowmap[before] = (int32_t)r;
+    place_row<XT>(a, before, r, lane);
+  } else {
+    const int64_t i = total + (r - before);
+    if (i < (((int64_t)total + 255) & ~(int64_t)255)) zero_place<XT>(a, i, lane);
+    if (r < a.R.m) zero_outputs<XT>(a, r, lane);
+  }
+  if (r0 == 0 && threadIdx.x == 0) *live_out = total;
 }
 
 // float32 table -> three bf16 planes [3][count], 8 values a thread.
@@ -746,40 +806,47 @@ __global__ void __launch_bounds__(kRowThreads) split_table_kernel(const float* _
 // joining the tiles' statistics
 // ---------------------------------------------------------------------------------------------
 // lse_i = top / tau + log sum_j S_j exp((M_j - top) / tau) over the row's parts, and for the cross
-// entropy loss_i = lse_i - s_target / tau. CTA = 32 rows x 8 lanes over the parts.
-__global__ void __launch_bounds__(256) join_stats_kernel(const float2* __restrict__ part, int parts, int64_t m_pad,
-                                                         const int32_t* __restrict__ live_p,
-                                                         const int32_t* __restrict__ rowmap,
-                                                         const float* __restrict__ st, float inv_tau, float* loss,
-                                                         float* lse_out) {
-  __shared__ float2 red[8][32];
+// entropy loss_i = lse_i - s_target / tau. CTA = 32 rows x 32 lanes over the parts, four parts in flight
+// per lane (a lane's chain over 250 / 32 parts is what the call costs when there are few rows).
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads) join_stats_kernel(const float2* __restrict__ part, int parts,
+                                                                  int64_t m_pad, const int32_t* __restrict__ live_p,
+                                                                  const int32_t* __restrict__ rowmap,
+                                                                  const float* __restrict__ st, float inv_tau,
+                                                                  float* loss, float* lse_out) {
+  __shared__ float2 red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int live = *live_p;
   const int64_t i = (int64_t)blockIdx.x * 32 + tx;
   if ((int64_t)blockIdx.x * 32 >= live) return;
   float mx = -INFINITY, sum = 0.0f;
   if (i < live) {
-    for (int j = ty; j < parts; j += 8) {
-      const float2 p = part[(int64_t)j * m_pad + i];
-      const float top = fmaxf(mx, p.x);
+    for (int j0 = ty; j0 < parts; j0 += 128) {
+      float2 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        p[u] = j0 + 32 * u < parts ? part[(int64_t)(j0 + 32 * u) * m_pad + i] : make_float2(-INFINITY, 0.0f);
+      const float top = fmaxf(fmaxf(mx, fmaxf(p[0].x, p[1].x)), fmaxf(p[2].x, p[3].x));
       const float ref = top == -INFINITY ? 0.0f : top;
-      sum = sum * expf((mx - ref) * inv_tau) + p.y * expf((p.x - ref) * inv_tau);
+      sum *= expf((mx - ref) * inv_tau);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += p[u].y * expf((p[u].x - ref) * inv_tau);
       mx = top;
     }
   }
   red[ty][tx] = make_float2(mx, sum);
   __syncthreads();
-  if (ty == 0 && i < live) {
-    float top = -INFINITY, s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, red[j][tx].x);
-    const float ref = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s += red[j][tx].y * expf((red[j][tx].x - ref) * inv_tau);
+  // warp ty joins row ty's 32 lanes
+  const float2 p = red[tx][ty];
+  const float top = warp_max(p.x);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  const float s = warp_sum(p.y * expf((p.x - ref) * inv_tau));
+  const int64_t row = (int64_t)blockIdx.x * 32 + ty;
+  if (tx == 0 && row < live) {
     const float l = top * inv_tau + logf(s);
-    const int64_t r = rowmap[i];
+    const int64_t r = rowmap[row];
     lse_out[r] = l;
-    if (st) loss[r] = l - st[i] * inv_tau;
+    if (st) loss[r] = l - st[row] * inv_tau;
   }
 }
 

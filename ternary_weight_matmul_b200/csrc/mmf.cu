@@ -1015,8 +1015,27 @@ mmf_status head_tc_pass(const void* x, mmf_dtype xdt, int nb, int d, const float
 // make the two products' tiles equally long.
 constexpr size_t kLossPieceBytes = (size_t)512 << 20;
 constexpr int64_t kLossMinPiece = 4096;
-constexpr int kLossSplitTiles = 74;   // K splits are added until a product has about this many tiles
-constexpr int kLossSplitBlocks = 8;   // ... of at least this many 64-wide k-blocks
+constexpr int kLossPairs = 74;         // CTA pairs at work at once
+constexpr int kLossSplitBlocks = 8;    // a K split has at least this many 64-wide k-blocks
+constexpr int kLossTileBlocks = 4;     // a tile's epilogue, in k-blocks' time
+constexpr int kLossMaxSplit = 64;
+
+// K splits of a product with `tiles` tiles of `kb` k-blocks, where the tiles alone leave pairs idle:
+// the number with the shortest run of tiles on one pair, the smallest of those (every split is a
+// float32 partial to write and add).
+int32_t loss_splits(int64_t tiles, int64_t kb) {
+  if (tiles >= kLossPairs) return 1;
+  int32_t best = 1;
+  int64_t cost = INT64_MAX;
+  for (int32_t s = 1; s <= kLossMaxSplit && (s == 1 || kb / s >= kLossSplitBlocks); ++s) {
+    const int64_t c = (tiles * s + kLossPairs - 1) / kLossPairs * ((kb + s - 1) / s + kLossTileBlocks);
+    if (c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
 
 struct LossPlan {
   int64_t m_pad;
@@ -1076,13 +1095,9 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   L.piece = (v256 / 256 + L.pieces - 1) / L.pieces * 256;  // even pieces
   L.pieces = (int32_t)((vocab + L.piece - 1) / L.piece);
   L.ldg = L.piece;
-  const auto splits = [](int64_t tiles, int64_t kb) {
-    const int64_t want = tiles > 0 ? (kLossSplitTiles + tiles - 1) / tiles : 1;
-    return (int32_t)std::max<int64_t>(1, std::min<int64_t>({want, kb / kLossSplitBlocks, 64}));
-  };
   const int64_t nt = hl::cdiv(d, hl::BN);
-  L.dx_split = splits(L.m_pad / hl::BM * nt, L.piece / hl::BK);
-  L.dt_split = splits(hl::cdiv(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
+  L.dx_split = loss_splits(L.m_pad / hl::BM * nt, L.piece / hl::BK);
+  L.dt_split = loss_splits(hl::cdiv(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
   L.g = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pg * M * L.ldg * 2));
   L.dxp = reinterpret_cast<float*>(take((size_t)L.pieces * L.dx_split * M * d * 4));
   if (L.dt_split > 1) L.dtp = reinterpret_cast<float*>(take((size_t)L.dt_split * vocab * d * 4));
@@ -1148,7 +1163,6 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, hl
     launch_k(hl::teacher_rows_kernel, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, a.teacher, a.m, L.flags);
     ++*launches;
   }
-  launch_k(hl::live_rows_kernel, dim3(1), dim3(hl::kScanThreads), 0, st, R, L.rowmap, L.live);
   ga.R = R;
   ga.rowmap = L.rowmap;
   ga.live = L.live;
@@ -1156,9 +1170,17 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, hl
   ga.d = a.d;
   ga.m_pad = L.m_pad;
   ga.xg = L.xg;
-  if (a.xdt == MMF_F32) launch_k(hl::gather_rows_kernel<MMF_F32>, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, ga);
-  else launch_k(hl::gather_rows_kernel<MMF_BF16>, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, ga);
-  *launches += 2;
+  const dim3 grid(row_ctas), block(hl::kRowThreads);
+  if (a.m <= hl::kOneLaunchRows) {
+    if (a.xdt == MMF_F32) launch_k(hl::place_rows_kernel<MMF_F32>, grid, block, 0, st, ga, L.rowmap, L.live);
+    else launch_k(hl::place_rows_kernel<MMF_BF16>, grid, block, 0, st, ga, L.rowmap, L.live);
+    ++*launches;
+  } else {
+    launch_k(hl::live_rows_kernel, dim3(1), dim3(hl::kScanThreads), 0, st, R, L.rowmap, L.live);
+    if (a.xdt == MMF_F32) launch_k(hl::gather_rows_kernel<MMF_F32>, grid, block, 0, st, ga);
+    else launch_k(hl::gather_rows_kernel<MMF_BF16>, grid, block, 0, st, ga);
+    *launches += 2;
+  }
   const void* table = a.table;
   if (a.tdt == MMF_F32) {
     const int64_t count = (int64_t)a.vocab * a.d;
@@ -1208,7 +1230,7 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
   P.st = L.st;
   P.tgt = ga.tgt;
   loss_launch<hl::kStats, true>(P, *di, st);
-  launch_k(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(256), 0, st, (const float2*)L.part, L.parts,
+  launch_k(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
            L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
            1.0f / a.tau, loss, lse);
   launches += 2;
@@ -1332,10 +1354,13 @@ void rms_fwd_launch(const rms::Args& a, const RmsPlan& p, const DevInfo& di, cud
   else if (p.chunks == 2) launch_k(rms::rms_fwd_kernel<XT, YT, 2, 1>, grid(1), dim3(p.threads), 0, st, a);
   else launch_k(rms::rms_fwd_kernel<XT, YT, 4, 1>, grid(1), dim3(p.threads), 0, st, a);
 }
+// rows per turn of the backward: as many as keep the raw chunks of two turns in registers
+template <mmf_dtype XT, mmf_dtype GT>
+constexpr int kRmsRows = XT == MMF_BF16 && GT == MMF_BF16 ? 3 : 2;
 template <mmf_dtype XT, mmf_dtype GT>
 void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t st) {
   const dim3 grid((unsigned)ctas);
-  if (p.chunks == 1) launch_k(rms::rms_bwd_kernel<XT, GT, 1, 2>, grid, dim3(p.threads), 0, st, a);
+  if (p.chunks == 1) launch_k(rms::rms_bwd_kernel<XT, GT, 1, kRmsRows<XT, GT>>, grid, dim3(p.threads), 0, st, a);
   else if (p.chunks == 2) launch_k(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
   else launch_k(rms::rms_bwd_kernel<XT, GT, 4, 1>, grid, dim3(p.threads), 0, st, a);
 }
@@ -2346,7 +2371,7 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
   a.xdt = x_dtype; a.dydt = dy_dtype; a.odt = x_dtype; a.m = m; a.d = d; a.eps = eps;
   LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (2.0 * dsize(x_dtype) + dsize(dy_dtype)), st);
   const RmsPlan p = rms_plan(d, {x, dy, dx, norm_w});
-  const int rows = p.vec && p.chunks == 1 ? 2 : 1;
+  const int rows = !p.vec || p.chunks != 1 ? 1 : x_dtype == MMF_BF16 && dy_dtype == MMF_BF16 ? 3 : 2;
   const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * 4, kRmsMaxParts});
   if (!p.vec) {
     launch_k(rms::rms_bwd_any_kernel, dim3((unsigned)ctas), dim3(rms::kGenThreads), 0, st, a);

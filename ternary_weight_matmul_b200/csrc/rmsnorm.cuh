@@ -134,6 +134,28 @@ __global__ void __launch_bounds__(kMaxThreads) rms_fwd_kernel(const Args a) {
   }
 }
 
+// Eight values as loaded: 16 bytes of bf16 or 32 of float32.
+template <mmf_dtype DT> struct Raw8 { uint4 v[DT == MMF_F32 ? 2 : 1]; };
+template <mmf_dtype DT>
+__device__ __forceinline__ void load_raw(const void* p, int64_t idx, Raw8<DT>& r) {
+  const uint4* s = reinterpret_cast<const uint4*>(reinterpret_cast<const typename Elem<DT>::T*>(p) + idx);
+  r.v[0] = s[0];
+  if (DT == MMF_F32) r.v[DT == MMF_F32 ? 1 : 0] = s[1];
+}
+template <mmf_dtype DT>
+__device__ __forceinline__ float raw_at(const Raw8<DT>& r, int e) {
+  if (DT == MMF_F32) {
+    const uint4& q = r.v[DT == MMF_F32 ? e >> 2 : 0];
+    const uint32_t w = (e & 3) == 0 ? q.x : (e & 3) == 1 ? q.y : (e & 3) == 2 ? q.z : q.w;
+    return __uint_as_float(w);
+  }
+  const uint4& q = r.v[0];
+  const uint32_t w = (e >> 1) == 0 ? q.x : (e >> 1) == 1 ? q.y : (e >> 1) == 2 ? q.z : q.w;
+  return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+}
+
+// The next turn's rows are loaded before this turn's block reduction, so that loads are in flight
+// across its barrier.
 template <mmf_dtype XT, mmf_dtype GT, int NC, int R>
 __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
   __shared__ float red[2][2 * R][16];
@@ -147,33 +169,43 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
     for (int e = 0; e < 8; ++e) { w[j][e] = 1.0f; dw[j][e] = 0.0f; }
     if (a.w && c < nck) load8<MMF_F32>(a.w, 8 * c, w[j]);
   }
-  int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.m; r0 += (int64_t)gridDim.x * R, turn ^= 1) {
-    float x[R][NC][8], g[R][NC][8], s[2 * R];
+  Raw8<XT> x[R][NC], xn[R][NC];
+  Raw8<GT> g[R][NC], gn[R][NC];
+  const auto fetch = [&](int64_t r0) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int c = j * T + (int)threadIdx.x;
+        xn[r][j] = Raw8<XT>{};
+        gn[r][j] = Raw8<GT>{};
         if (r0 + r < a.m && c < nck) {
-          load8<XT>(a.x, (r0 + r) * a.d + 8 * c, x[r][j]);
-          load8<GT>(a.dy, (r0 + r) * a.d + 8 * c, g[r][j]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[r][j][e] = g[r][j][e] = 0.0f;
+          load_raw<XT>(a.x, (r0 + r) * a.d + 8 * c, xn[r][j]);
+          load_raw<GT>(a.dy, (r0 + r) * a.d + 8 * c, gn[r][j]);
         }
       }
+  };
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * R;
+  fetch((int64_t)blockIdx.x * R);
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.m; r0 += step, turn ^= 1) {
+    float s[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       s[r] = s[R + r] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NC; ++j)
+      for (int j = 0; j < NC; ++j) {
+        x[r][j] = xn[r][j];
+        g[r][j] = gn[r][j];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s[r] = fmaf(x[r][j][e], x[r][j][e], s[r]);
-          s[R + r] = fmaf(g[r][j][e] * w[j][e], x[r][j][e], s[R + r]);
+          const float xv = raw_at<XT>(x[r][j], e);
+          s[r] = fmaf(xv, xv, s[r]);
+          s[R + r] = fmaf(raw_at<GT>(g[r][j], e) * w[j][e], xv, s[R + r]);
         }
+      }
     }
+    fetch(r0 + step);
     block_sums<2 * R>(s, red[turn]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -187,8 +219,9 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dw[j][e] = fmaf(g[r][j][e] * rho, x[r][j][e], dw[j][e]);
-          o[e] = rho * (g[r][j][e] * w[j][e]) - k * x[r][j][e];
+          const float xv = raw_at<XT>(x[r][j], e), gv = raw_at<GT>(g[r][j], e);
+          dw[j][e] = fmaf(gv * rho, xv, dw[j][e]);
+          o[e] = rho * (gv * w[j][e]) - k * xv;
         }
         store8<XT>(a.out, (r0 + r) * a.d + 8 * c, o);
       }
