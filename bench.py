@@ -67,7 +67,8 @@ def parse():
     ap.add_argument("--no-extra", action="store_true", help="skip the 1.3B prefill, sweeps and next-row kernels")
     ap.add_argument("--decode-steps", type=int, default=256)
     ap.add_argument("--case", default=None,
-                    choices=["gemm", "scan", "block", "norm", "decode", "head", "hgrn2", "scan_bwd", "lin_bwd"],
+                    choices=["gemm", "scan", "block", "norm", "decode", "head", "hgrn2", "scan_bwd", "lin_bwd", "rmsnorm", "xent",
+                             "distill"],
                     help="run one kernel case and print its device time (for profiler captures)")
     ap.add_argument("--m", type=int, default=16384)
     ap.add_argument("--n", type=int, default=5632)
@@ -79,6 +80,7 @@ def parse():
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--vocab", type=int, default=32000)
     ap.add_argument("--heads", type=int, default=8)
+    ap.add_argument("--top-k", type=int, default=64)
     ap.add_argument("--dtype", default="bf16", choices=["bf16", "f32"])
     ap.add_argument("--iters", type=int, default=5)
     ap.add_argument("--engine", default="auto", choices=["auto", "tensor", "simt"])
@@ -916,6 +918,10 @@ def run_case(a) -> int:
         python bench.py --case block --m 16384 --d 1024 --inner 2816
         python bench.py --case decode --b 1 --d 2560 --inner 7040 --layers 4
         python bench.py --case head --b 8 --d 2560 --vocab 32000 --iters 1
+        python bench.py --case xent --m 16384 --d 1024 --vocab 32000
+        python bench.py --case distill --m 16384 --d 1024 --vocab 32000 --top-k 64
+        python bench.py --case rmsnorm --m 16384 --d 1024
+    (the last three forward + backward)
     """
     import torch
 
@@ -1009,6 +1015,30 @@ def run_case(a) -> int:
         def run():
             return mmf.bitlinear_backward(x, nw, w, qq, deq, dy)
         work, unit = 4.0 * a.m * a.n * a.k, "TFLOP/s (dr + dW)"
+    elif a.case == "rmsnorm":
+        x = torch.randn(a.m, a.d, generator=g, device=dev).to(dt)
+        dy = torch.randn(a.m, a.d, generator=g, device=dev).to(dt)
+        nw = torch.ones(a.d, device=dev)
+
+        def run():
+            return mmf.rmsnorm_fwd(x, nw), mmf.rmsnorm_backward(x, nw, dy)
+        work, unit = float(5 * a.m * a.d * (4 if dt == torch.float32 else 2)), "GB/s"
+    elif a.case in ("xent", "distill"):
+        table = (torch.randn(a.vocab, a.d, generator=g, device=dev) * 0.02).to(dt)
+        x = torch.randn(a.m, a.d, generator=g, device=dev).to(dt)
+        dl = torch.full((a.m,), 1.0 / a.m, device=dev)
+        targets = torch.randint(0, a.vocab, (a.m,), generator=g, device=dev).to(torch.int32)
+        step = max(1, a.vocab // a.top_k - 1)
+        t_ids = ((targets[:, None] + step * torch.arange(a.top_k, device=dev)) % a.vocab).to(torch.int32)
+        t_logits = 4.0 * torch.randn(a.m, a.top_k, generator=g, device=dev)
+
+        def run():
+            if a.case == "xent":
+                _, lse = mmf.lm_head_xent_fwd(x, table, targets)
+                return mmf.lm_head_xent_backward(x, table, targets, lse, dl)
+            _, lse, s_top = mmf.lm_head_distill_fwd(x, table, t_ids, t_logits)
+            return mmf.lm_head_distill_backward(x, table, t_ids, t_logits, lse, s_top, dl)
+        work, unit = 8.0 * a.m * a.vocab * a.d, "TFLOP/s (logits twice, dx, dtable)"
     else:  # block
         blk = blocks_of(a.d, a.inner, 1)[0]
         x = torch.randn(1, a.m, a.d, generator=g, device=dev).to(dt)

@@ -78,8 +78,8 @@ typedef enum {
   MMF_OP_HEAD = 6,      /* mmf_lm_head_argmax: inner = vocabulary size            */
   MMF_OP_BITLINEAR_BWD = 7, /* mmf_bitlinear_backward: m rows, d = K, inner = N     */
   MMF_OP_RMSNORM_BWD = 8,  /* mmf_rmsnorm_backward: m rows, d                      */
-  /* the head losses: m rows, d, inner = vocabulary size, n_layers = bit 0 set when x is float32 and
-   * bit 1 set when the table is */
+  /* the head losses: m rows, d, inner = vocabulary size, n_layers = (x is float32 ? 1 : 0) +
+   * (the table is float32 ? 2 : 0) + 4 * top_k (distillation; 0 for the cross entropy) */
   MMF_OP_HEAD_LOSS = 9,     /* mmf_lm_head_xent_fwd, mmf_lm_head_distill_fwd           */
   MMF_OP_HEAD_LOSS_BWD = 10 /* mmf_lm_head_xent_backward, mmf_lm_head_distill_backward */
 } mmf_op;
@@ -301,7 +301,7 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
  *   targets [m] int32. A target outside [0, vocab) leaves its row out: loss = lse = 0, and nothing of
  *           that row is computed with (it may hold anything).
  *   loss, lse [m] float32 out. Sums and mean over the rows are the caller's.
- *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, type bits). m = 0 is a no-op.
+ *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, n_layers as at mmf_op). m = 0 is a no-op.
  * bf16 tensor cores with float32 accumulation and softmax statistics; a float32 operand enters as
  * three bf16 planes that hold it exactly, so float32 inputs give float32-accurate results.
  * Deterministic. */
@@ -316,7 +316,7 @@ mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int
  * The logits are computed again in pieces of the vocabulary; one piece's g is held in the workspace
  * (about 512 MB at most up to 65536 rows). g is rounded to bf16 once where x and table are bf16, and
  * kept as three exact planes otherwise; both products accumulate in float32.
- *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, type bits). m = 0 zeroes dtable. */
+ *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, n_layers as at mmf_op). m = 0 zeroes dtable. */
 mmf_status mmf_lm_head_xent_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                      mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, const float* lse,
                                      const float* dloss, void* dx, void* dtable, void* ws, size_t ws_bytes,
@@ -332,7 +332,7 @@ mmf_status mmf_lm_head_xent_backward(const void* x, mmf_dtype x_dtype, int64_t m
  *   ids (0 for entries that are not valid), which the backward takes.
  * A row with no valid entry is left out as a row without target is (zeros). Entries of one row may
  * name one id; their q add up in the gradient. The factor temperature^2 some use is the caller's.
- *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, type bits). m = 0 is a no-op. */
+ *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, n_layers as at mmf_op). m = 0 is a no-op. */
 mmf_status mmf_lm_head_distill_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                    mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids, const void* t_logits,
                                    mmf_dtype t_dtype, int32_t top_k, float temperature, float* loss, float* lse,
@@ -340,7 +340,7 @@ mmf_status mmf_lm_head_distill_fwd(const void* x, mmf_dtype x_dtype, int64_t m, 
 
 /* Its gradients: g_rv = dloss[r] / temperature (exp(s_rv / temperature - lse[r]) - sum_{j: id = v} q_rj),
  * dx = g table, dtable = g^T x as above (the teacher's entries are computed whole in float32 before
- * their one rounding).  ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, type bits). */
+ * their one rounding).  ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, n_layers as at mmf_op). */
 mmf_status mmf_lm_head_distill_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                         mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids,
                                         const void* t_logits, mmf_dtype t_dtype, int32_t top_k, float temperature,

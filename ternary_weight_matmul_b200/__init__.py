@@ -724,7 +724,7 @@ def lm_head_distill_fwd(x: torch.Tensor, table: torch.Tensor, t_ids: torch.Tenso
     lse = torch.empty(m, dtype=torch.float32, device=x.device)
     s_top = torch.empty(m, k, dtype=torch.float32, device=x.device)
     with _on(x.device):
-        ws = _scratch(MMF_OP_HEAD_LOSS, m, d, vocab, bits, x.device)
+        ws = _scratch(MMF_OP_HEAD_LOSS, m, d, vocab, bits + 4 * k, x.device)
         _check(lib().mmf_lm_head_distill_fwd(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(), _dt(table.dtype),
                                              vocab, t_ids.data_ptr(), t_logits.data_ptr(), _dt(t_logits.dtype), k,
                                              temperature, loss.data_ptr(), lse.data_ptr(), s_top.data_ptr(),
@@ -746,7 +746,7 @@ def lm_head_distill_backward(x: torch.Tensor, table: torch.Tensor, t_ids: torch.
     dx = torch.empty_like(x) if want_dx else None
     dtable = torch.empty_like(table) if want_dtable else None
     with _on(x.device):
-        ws = _scratch(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, bits, x.device)
+        ws = _scratch(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, bits + 4 * k, x.device)
         _check(lib().mmf_lm_head_distill_backward(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(),
                                                   _dt(table.dtype), vocab, t_ids.data_ptr(), t_logits.data_ptr(),
                                                   _dt(t_logits.dtype), k, temperature, lse.data_ptr(),

@@ -80,6 +80,12 @@ struct Params {
   const float* c;       // [m_pad] dloss / tau (kGrad)
   float2* part;         // [2 * column tiles][m_pad] (maximum, sum) (kStats)
   float* st;            // [m_pad] target logit (kStats)
+  // distillation (kStats): the teacher's entries of every row in order of their ids
+  const int2* top;      // [m][top_k] (id, entry), or nullptr
+  const uint16_t* top_start;  // [2 * column tiles][m_pad] the row's first entry in the tile's half
+  const int32_t* rowmap;      // [m_pad] row of each live row
+  float* s_top;         // [m][top_k] out: the student's logits at the entries
+  int32_t top_k;
   Prods fwd, dxp, dtp;
   int32_t dx_split, dx_plane0;  // K splits of dx in this launch (0: no dx) and its first partial plane
   int32_t dt_split;             // K splits of dT (0: no dT)
@@ -155,6 +161,11 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_des
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+  return r;
 }
 // 2^v by the hardware approximation (2 ulp over the range the softmax needs; 0 for -inf).
 __device__ __forceinline__ float ex2(float v) {
@@ -482,6 +493,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         for (int e = 0; e < W; ++e) s4[e & 3] += ex2(fmaf(sum[e], P.scale, off));
         if (row < live)
           P.part[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+        if (P.top) {
+          // the logits at the teacher's ids, while they are here: a group of 32 columns that holds one
+          // of the warp's entries goes through the warp's staging rows, where it can be indexed
+          int pos = P.top_k;
+          int64_t base = 0;
+          int2 ent = make_int2(0x7fffffff, 0);
+          if (row < live) {
+            const int32_t r = P.rowmap[row];
+            base = (int64_t)r * P.top_k;
+            pos = P.top_start[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + r];
+            if (pos < P.top_k) ent = P.top[base + pos];
+          }
+#pragma unroll
+          for (int c0 = 0; c0 < W; c0 += 32) {
+            const int begin = col0 + c0;
+            if (!__any_sync(0xffffffffu, ent.x < begin + 32)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), __float_as_uint(sum[FLUSH ? c0 + 4 * j : 0]),
+                           __float_as_uint(sum[FLUSH ? c0 + 4 * j + 1 : 0]), __float_as_uint(sum[FLUSH ? c0 + 4 * j + 2 : 0]),
+                           __float_as_uint(sum[FLUSH ? c0 + 4 * j + 3 : 0]));
+            while (ent.x < begin + 32) {  // at most top_k entries; a row reads what its own thread wrote
+              const uint32_t c = (uint32_t)(ent.x - begin);
+              P.s_top[base + ent.y] = ld_shared_f32(stg_row + (((c >> 2) << 4) ^ swz) + ((c & 3u) << 2));
+              ent = ++pos < P.top_k ? P.top[base + pos] : make_int2(0x7fffffff, 0);
+            }
+          }
+        }
       } else if (MODE == kGrad) {
         // pad rows have c = lse = 0: zeros, which the products over the live rows rely on
         const float c = P.c[row], lse2 = P.lse[row] * kLog2e;
@@ -898,20 +937,6 @@ __device__ __forceinline__ bool teacher_valid(const Teacher& t, int64_t at, floa
   return (uint32_t)t.ids[at] < (uint32_t)t.vocab && !(logit == -INFINITY);
 }
 
-// flags[r] = 1 when row r has a valid entry. One warp per row.
-__global__ void __launch_bounds__(kRowThreads) teacher_rows_kernel(const Teacher t, int64_t m, uint8_t* __restrict__ flags) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  if (r >= m) return;
-  bool any = false;
-  for (int j = lane; j < t.k; j += 32) {
-    float l;
-    any |= teacher_valid(t, r * t.k + j, l);
-  }
-  any = __any_sync(0xffffffffu, any);
-  if (lane == 0) flags[r] = any ? 1 : 0;
-}
-
 // The row's teacher distribution over its valid entries: top = the largest valid logit, total = sum
 // exp((t_j - top) / tau). Whole warp; the differences are taken before the division by tau, so that
 // logits near the type's lowest value stay finite.
@@ -935,76 +960,125 @@ __device__ __forceinline__ void teacher_softmax(const Teacher& t, int64_t r, int
   total = warp_sum(total);
 }
 
-constexpr int kDistillThreads = 256;
-
-// One CTA per row: s_j = x . T[id_j] for the valid entries (float32 accumulation, a warp per entry),
-// then loss = sum_j q_j (log q_j - s_j / tau + lse). Rows that are not live get zeros.
-template <mmf_dtype XT, mmf_dtype TT>
-__global__ void __launch_bounds__(kDistillThreads) distill_loss_kernel(const Teacher t, const uint8_t* __restrict__ flags,
-                                                                       const void* __restrict__ x,
-                                                                       const void* __restrict__ table, int d,
-                                                                       const float* __restrict__ lse, float* loss,
-                                                                       float* s_top) {
-  extern __shared__ __align__(16) float xs[];  // [d]
-  __shared__ float sj[MAX_TOP];
-  const int64_t r = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nck = d >> 3;
-  if (!flags[r]) {  // uniform across the CTA; loss and lse are zeroed by the gather
-    for (int j = threadIdx.x; j < t.k; j += kDistillThreads) s_top[r * t.k + j] = 0.0f;
-    return;
+constexpr int kTeacherRows = 32;      // rows per CTA, one warp each
+constexpr int kTeacherTiles = 128;    // tile halves per turn
+// Per row: its live flag (it has a valid entry), and its entries in order of their ids (equal ids in
+// order of the entries), entries that are not valid last with id 2^31 - 1. The place of an entry is the
+// number of entries before it, counted over the row in shared memory.
+//   starts (forward): start[h][r] = entries with an id below 128 h, so that the tile half at columns
+//     128 h finds its own without a search, and zeros in s_top at entries that are not valid;
+//   q (backward): the teacher's weight of every entry, in the same order.
+__global__ void __launch_bounds__(kTeacherRows * 32) teacher_rows_kernel(const Teacher t, int64_t m, int64_t m_pad,
+                                                                         int halves, uint8_t* __restrict__ flags,
+                                                                         int2* __restrict__ top,
+                                                                         uint16_t* __restrict__ start,
+                                                                         float* __restrict__ s_top,
+                                                                         float* __restrict__ q) {
+  __shared__ __align__(16) int32_t ids[kTeacherRows][MAX_TOP];
+  __shared__ uint16_t turn[kTeacherTiles][kTeacherRows + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = (int64_t)blockIdx.x * kTeacherRows, r = r0 + warp;
+  constexpr int PER = MAX_TOP / 32;
+  constexpr int32_t kNone = 0x7fffffff;
+  int32_t id[PER];
+  int place[PER];
+  bool any = false;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int j = u * 32 + lane;
+    id[u] = kNone;
+    if (r < m && j < t.k) {
+      float l;
+      const bool valid = teacher_valid(t, r * t.k + j, l);
+      if (valid) id[u] = t.ids[r * t.k + j];
+      any |= valid;
+      if (s_top && !valid) s_top[r * t.k + j] = 0.0f;
+    }
+    if (u * 32 < t.k) ids[warp][j] = id[u];  // past the row's entries: no id, counted by nobody
   }
-  for (int c = threadIdx.x; c < d; c += kDistillThreads) xs[c] = load_as_float(x, r * d + c, XT);
-  __syncthreads();
-  for (int j = warp; j < t.k; j += kDistillThreads / 32) {
-    float l, acc = 0.0f;
-    const bool valid = teacher_valid(t, r * t.k + j, l);
-    if (valid) {
-      const int64_t row = (int64_t)t.ids[r * t.k + j] * d;
-      for (int c = lane; c < nck; c += 32) {
-        const float4 u = reinterpret_cast<const float4*>(xs)[2 * c], w = reinterpret_cast<const float4*>(xs)[2 * c + 1];
-        if (TT == MMF_F32) {
-          const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(table) + row) + 2 * c;
-          const float4 a = p[0], b = p[1];
-          acc = fmaf(a.x, u.x, acc); acc = fmaf(a.y, u.y, acc); acc = fmaf(a.z, u.z, acc); acc = fmaf(a.w, u.w, acc);
-          acc = fmaf(b.x, w.x, acc); acc = fmaf(b.y, w.y, acc); acc = fmaf(b.z, w.z, acc); acc = fmaf(b.w, w.w, acc);
-        } else {
-          const uint4 p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(table) + row)[c];
-          acc = fmaf(__uint_as_float(p.x << 16), u.x, acc); acc = fmaf(__uint_as_float(p.x & 0xffff0000u), u.y, acc);
-          acc = fmaf(__uint_as_float(p.y << 16), u.z, acc); acc = fmaf(__uint_as_float(p.y & 0xffff0000u), u.w, acc);
-          acc = fmaf(__uint_as_float(p.z << 16), w.x, acc); acc = fmaf(__uint_as_float(p.z & 0xffff0000u), w.y, acc);
-          acc = fmaf(__uint_as_float(p.w << 16), w.z, acc); acc = fmaf(__uint_as_float(p.w & 0xffff0000u), w.w, acc);
+  any = __any_sync(0xffffffffu, any);
+  if (r < m && lane == 0) flags[r] = any ? 1 : 0;
+  __syncwarp();
+  if (r < m) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int j = u * 32 + lane;
+      place[u] = 0;
+      if (u * 32 < t.k)
+        for (int i = 0; i < t.k; i += 4) {
+          const int4 o = *reinterpret_cast<const int4*>(&ids[warp][i]);
+          const int32_t o4[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) place[u] += o4[e] < id[u] || (o4[e] == id[u] && i + e < j) ? 1 : 0;
+        }
+    }
+    float best = 0.0f, total = 1.0f;
+    if (q) teacher_softmax(t, r, lane, best, total);
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int j = u * 32 + lane;
+      if (j < t.k) {
+        ids[warp][place[u]] = id[u];
+        top[r * t.k + place[u]] = make_int2(id[u], j);
+        if (q) {
+          float l;
+          const bool valid = teacher_valid(t, r * t.k + j, l);
+          q[r * t.k + place[u]] = valid ? expf((l - best) * t.inv_tau) / total : 0.0f;
         }
       }
-      acc = warp_sum(acc);
-    }
-    if (lane == 0) {
-      sj[j] = acc;
-      s_top[r * t.k + j] = acc;
     }
   }
-  __syncthreads();
-  if (warp == 0) {
-    float top, total, sum = 0.0f;
-    teacher_softmax(t, r, lane, top, total);
-    const float log_total = logf(total), L = lse[r];
-    for (int j = lane; j < t.k; j += 32) {
-      float l;
-      if (teacher_valid(t, r * t.k + j, l)) {
-        const float e = (l - top) * t.inv_tau, q = expf(e) / total;
-        // an entry whose q underflows adds nothing (0 log 0 = 0); NaN goes through
-        if (!(q == 0.0f)) sum += q * ((e - log_total) - (sj[j] * t.inv_tau - L));
+  if (!start) return;  // uniform
+  __syncwarp();
+  for (int h0 = 0; h0 < halves; h0 += kTeacherTiles) {
+    for (int h = lane; h < kTeacherTiles; h += 32) {
+      int lo = 0, hi = r < m ? t.k : 0;
+      const int64_t bound = (int64_t)(h0 + h) * (BN / 2);
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (ids[warp][mid] < bound) lo = mid + 1;
+        else hi = mid;
       }
+      turn[h][warp] = (uint16_t)lo;
     }
-    sum = warp_sum(sum);
-    if (lane == 0) loss[r] = sum;
+    __syncthreads();
+    for (int h = warp; h < kTeacherTiles && h0 + h < halves; h += kTeacherRows)
+      if (r0 + lane < m_pad) start[(int64_t)(h0 + h) * m_pad + r0 + lane] = turn[h][lane];
+    __syncthreads();
   }
 }
 
-// The teacher's share of g for the piece [v0, v0 + vn): for every valid entry of live row i with its
-// id in the piece, g[i][id] = c (exp(s_j / tau - lse) - sum of q over the row's entries with that id),
+// loss = sum_j q_j (log q_j - s_j / tau + lse) of the live rows. One warp per row.
+__global__ void __launch_bounds__(kRowThreads) distill_loss_kernel(const Teacher t, int64_t m,
+                                                                   const uint8_t* __restrict__ flags,
+                                                                   const float* __restrict__ lse,
+                                                                   const float* __restrict__ s_top, float* loss) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (r >= m || !flags[r]) return;  // the gather has zeroed the row's loss
+  float top, total, sum = 0.0f;
+  teacher_softmax(t, r, lane, top, total);
+  const float log_total = logf(total), L = lse[r];
+  for (int j = lane; j < t.k; j += 32) {
+    float l;
+    if (teacher_valid(t, r * t.k + j, l)) {
+      const float e = (l - top) * t.inv_tau, q = expf(e) / total;
+      // an entry whose q underflows adds nothing (0 log 0 = 0); NaN goes through
+      if (!(q == 0.0f)) sum += q * ((e - log_total) - (s_top[r * t.k + j] * t.inv_tau - L));
+    }
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) loss[r] = sum;
+}
+
+// The teacher's share of g for the piece [v0, v0 + vn): for every entry of live row i with its id in
+// the piece, g[i][id] = c (exp(s_j / tau - lse) - sum of q over the row's entries with that id),
 // computed whole in float32 from the kept s_j and stored over the softmax part (so nothing is rounded
-// twice). One warp per row; entries with one id write one value.
-__global__ void __launch_bounds__(kRowThreads) teacher_grad_kernel(const Teacher t, const int32_t* __restrict__ live_p,
+// twice). One warp per row; the first entry of a run of equal ids writes.
+__global__ void __launch_bounds__(kRowThreads) teacher_grad_kernel(const int2* __restrict__ top,
+                                                                   const float* __restrict__ q, int k, float inv_tau,
+                                                                   const int32_t* __restrict__ live_p,
                                                                    const int32_t* __restrict__ rowmap,
                                                                    const float* __restrict__ s_top,
                                                                    const float* __restrict__ c_p,
@@ -1014,45 +1088,18 @@ __global__ void __launch_bounds__(kRowThreads) teacher_grad_kernel(const Teacher
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (i >= *live_p) return;
-  const int64_t r = rowmap[i];
-  float top, total;
-  teacher_softmax(t, r, lane, top, total);
+  const int64_t base = (int64_t)rowmap[i] * k;
   const float c = c_p[i], L = lse_p[i];
-  for (int j0 = 0; j0 < t.k; j0 += 32) {
-    const int j = j0 + lane;
-    float l = 0.0f;
-    const bool mine = j < t.k && teacher_valid(t, r * t.k + j, l) && t.ids[r * t.k + j] >= v0 &&
-                      t.ids[r * t.k + j] < v0 + vn;
-    const int id = mine ? t.ids[r * t.k + j] : -1;
-    // every entry of the row passes by once, in order
-    float q = 0.0f;
-    for (int b0 = 0; b0 < t.k; b0 += 32) {
-      const int b = b0 + lane;
-      float lb = 0.0f, qb = 0.0f;
-      int idb = -2;
-      if (b < t.k && teacher_valid(t, r * t.k + b, lb)) {
-        idb = t.ids[r * t.k + b];
-        qb = expf((lb - top) * t.inv_tau) / total;
-      }
-      for (int o = 0; o < 32; ++o) {
-        const int ido = __shfl_sync(0xffffffffu, idb, o);
-        const float qo = __shfl_sync(0xffffffffu, qb, o);
-        if (ido == id) q += qo;
-      }
-    }
-    if (mine) {
-      const float v = c * (expf(s_top[r * t.k + j] * t.inv_tau - L) - q);
-      __nv_bfloat16* o = g + i * ldg + (id - v0);
-      if (planes == 1) {
-        *o = __float2bfloat16_rn(v);
-      } else {
-        float p0, p1, p2;
-        split3(v, p0, p1, p2);
-        o[0] = __float2bfloat16_rn(p0);
-        o[m_pad * ldg] = __float2bfloat16_rn(p1);
-        o[2 * m_pad * ldg] = __float2bfloat16_rn(p2);
-      }
-    }
+  for (int p = lane; p < k; p += 32) {
+    const int2 e = top[base + p];
+    if (e.x < v0 || e.x >= v0 + vn || (p > 0 && top[base + p - 1].x == e.x)) continue;
+    float w = q[base + p];
+    for (int n = p + 1; n < k && top[base + n].x == e.x; ++n) w += q[base + n];
+    float v = c * (expf(s_top[base + e.y] * inv_tau - L) - w);
+    __nv_bfloat16* o = g + i * ldg + (e.x - v0);
+    if (planes == 1) *o = __float2bfloat16_rn(v);
+    else
+      for (int pl = 0; pl < PLANES; ++pl) o[pl * m_pad * ldg] = __float2bfloat16_rn(peel(v));
   }
 }
 

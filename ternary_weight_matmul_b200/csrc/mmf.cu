@@ -114,8 +114,6 @@ unsigned long long current_ctx_id() {
   return id;
 }
 
-constexpr int kHeadLossMaxD = 32768;  // hidden sizes of the head losses (a row fits shared memory)
-
 template <mmf_dtype ZT, mmf_dtype HT>
 cudaError_t scan_tile_attrs() {
   cudaError_t e = cudaSuccess;
@@ -155,10 +153,6 @@ cudaError_t head_loss_attrs() {
   set((const void*)hl::head_loss_kernel<hl::kGrad, true>, hl::SMEM_BYTES);
   set((const void*)hl::head_loss_kernel<hl::kProducts, false>, hl::SMEM_BYTES);
   set((const void*)hl::head_loss_kernel<hl::kProducts, true>, hl::SMEM_BYTES);
-  set((const void*)hl::distill_loss_kernel<MMF_F32, MMF_F32>, kHeadLossMaxD * 4);
-  set((const void*)hl::distill_loss_kernel<MMF_F32, MMF_BF16>, kHeadLossMaxD * 4);
-  set((const void*)hl::distill_loss_kernel<MMF_BF16, MMF_F32>, kHeadLossMaxD * 4);
-  set((const void*)hl::distill_loss_kernel<MMF_BF16, MMF_BF16>, kHeadLossMaxD * 4);
   return e;
 }
 
@@ -1019,6 +1013,7 @@ constexpr int kLossPairs = 74;         // CTA pairs at work at once
 constexpr int kLossSplitBlocks = 8;    // a K split has at least this many 64-wide k-blocks
 constexpr int kLossTileBlocks = 4;     // a tile's epilogue, in k-blocks' time
 constexpr int kLossMaxSplit = 64;
+constexpr int32_t kHeadLossMaxD = 32768;
 
 // K splits of a product with `tiles` tiles of `kb` k-blocks, where the tiles alone leave pairs idle:
 // the number with the shortest run of tiles on one pair, the smallest of those (every split is a
@@ -1050,6 +1045,9 @@ struct LossPlan {
   __nv_bfloat16* tp;        // table planes (float32 tables)
   float2* part;
   float* st;
+  int2* top;                // distillation: the teacher's entries in order of their ids
+  uint16_t* top_start;
+  float* q;
   int32_t* tgt;
   float *c, *lse;
   __nv_bfloat16* g;
@@ -1058,7 +1056,8 @@ struct LossPlan {
   size_t bytes;
 };
 
-LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bool backward, void* base) {
+LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bool backward, int32_t top_k,
+                   void* base) {
   LossPlan L;
   memset(&L, 0, sizeof(L));
   uint8_t* p = reinterpret_cast<uint8_t*>(base);
@@ -1075,7 +1074,10 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   const size_t M = (size_t)L.m_pad;
   L.live = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   L.rowmap = reinterpret_cast<int32_t*>(take(M * 4));
-  L.flags = take(M);
+  if (top_k > 0) {
+    L.flags = take(M);
+    L.top = reinterpret_cast<int2*>(take((size_t)m * top_k * sizeof(int2)));
+  }
   L.xg = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.px * M * d * 2));
   if (tf32) L.tp = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pt * vocab * d * 2));
   L.tgt = reinterpret_cast<int32_t*>(take(M * 4));
@@ -1083,9 +1085,11 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
     L.parts = 2 * hl::cdiv(vocab, hl::BN);
     L.part = reinterpret_cast<float2*>(take((size_t)L.parts * M * sizeof(float2)));
     L.st = reinterpret_cast<float*>(take(M * 4));
+    if (top_k > 0) L.top_start = reinterpret_cast<uint16_t*>(take((size_t)L.parts * M * sizeof(uint16_t)));
     L.bytes = off;
     return L;
   }
+  if (top_k > 0) L.q = reinterpret_cast<float*>(take((size_t)m * top_k * sizeof(float)));
   L.c = reinterpret_cast<float*>(take(M * 4));
   L.lse = reinterpret_cast<float*>(take(M * 4));
   const int64_t v256 = ((int64_t)vocab + 255) / 256 * 256;
@@ -1150,9 +1154,9 @@ mmf_status check_loss(const LossArgs& a, const char* name, bool distill, int32_t
 }
 
 // The launches before the products: live rows, gathered rows, table planes. Fills the parts of P
-// that every product launch shares.
-mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, hl::Params& P, const DevInfo& di,
-                     cudaStream_t st, int* launches) {
+// that every product launch shares. s_top: the forward's output, or nullptr.
+mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, float* s_top, hl::Params& P,
+                     const DevInfo& di, cudaStream_t st, int* launches) {
   const unsigned row_ctas = (unsigned)(L.m_pad / (hl::kRowThreads / 32));
   hl::Rows R;
   R.targets = a.targets;
@@ -1160,7 +1164,8 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, hl
   R.vocab = a.vocab;
   R.m = (int32_t)a.m;
   if (!a.targets) {
-    launch_k(hl::teacher_rows_kernel, dim3(row_ctas), dim3(hl::kRowThreads), 0, st, a.teacher, a.m, L.flags);
+    launch_k(hl::teacher_rows_kernel, dim3((unsigned)(L.m_pad / hl::kTeacherRows)), dim3(hl::kTeacherRows * 32), 0, st,
+             a.teacher, a.m, L.m_pad, L.parts, L.flags, L.top, L.top_start, s_top, L.q);
     ++*launches;
   }
   ga.R = R;
@@ -1211,7 +1216,8 @@ void loss_launch(const hl::Params& P, const DevInfo& di, cudaStream_t st) {
 
 mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top, void* ws, size_t ws_bytes,
                         cudaStream_t st) {
-  const LossPlan L = loss_plan(a.m, a.d, a.vocab, a.xdt == MMF_F32, a.tdt == MMF_F32, false, ws);
+  const LossPlan L = loss_plan(a.m, a.d, a.vocab, a.xdt == MMF_F32, a.tdt == MMF_F32, false,
+                              a.targets ? 0 : a.teacher.k, ws);
   MMF_TRY(check_ws(ws, ws_bytes, L.bytes));
   DevInfo* di;
   MMF_TRY(device_info(&di));
@@ -1224,27 +1230,24 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
   ga.zero1 = loss;
   ga.zero2 = lse;
   ga.tgt = a.targets ? L.tgt : nullptr;
-  MMF_TRY(loss_rows(a, L, ga, P, *di, st, &launches));
+  MMF_TRY(loss_rows(a, L, ga, s_top, P, *di, st, &launches));
   P.vn = a.vocab;
   P.part = L.part;
   P.st = L.st;
   P.tgt = ga.tgt;
+  P.top = L.top;
+  P.top_start = L.top_start;
+  P.rowmap = L.rowmap;
+  P.s_top = s_top;
+  P.top_k = a.teacher.k;
   loss_launch<hl::kStats, true>(P, *di, st);
   launch_k(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
            L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
            1.0f / a.tau, loss, lse);
   launches += 2;
   if (!a.targets) {
-    const size_t smem = (size_t)a.d * 4;
-    const dim3 grid((unsigned)a.m), block(hl::kDistillThreads);
-#define MMF_DISTILL(X_, T_)                                                                                      \
-  launch_k(hl::distill_loss_kernel<X_, T_>, grid, block, smem, st, a.teacher, (const uint8_t*)L.flags, a.x, a.table, \
-           a.d, (const float*)lse, loss, s_top)
-    if (a.xdt == MMF_F32 && a.tdt == MMF_F32) MMF_DISTILL(MMF_F32, MMF_F32);
-    else if (a.xdt == MMF_F32) MMF_DISTILL(MMF_F32, MMF_BF16);
-    else if (a.tdt == MMF_F32) MMF_DISTILL(MMF_BF16, MMF_F32);
-    else MMF_DISTILL(MMF_BF16, MMF_BF16);
-#undef MMF_DISTILL
+    launch_k(hl::distill_loss_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
+             a.teacher, a.m, (const uint8_t*)L.flags, (const float*)lse, (const float*)s_top, loss);
     ++launches;
   }
   g_launches.fetch_add(launches - 1);  // the timing scope counted one launch itself
@@ -1253,7 +1256,8 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
 
 mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top, const float* dloss, void* dx,
                          void* dtable, void* ws, size_t ws_bytes, cudaStream_t st) {
-  const LossPlan L = loss_plan(a.m, a.d, a.vocab, a.xdt == MMF_F32, a.tdt == MMF_F32, true, ws);
+  const LossPlan L = loss_plan(a.m, a.d, a.vocab, a.xdt == MMF_F32, a.tdt == MMF_F32, true,
+                              a.targets ? 0 : a.teacher.k, ws);
   MMF_TRY(check_ws(ws, ws_bytes, L.bytes));
   DevInfo* di;
   MMF_TRY(device_info(&di));
@@ -1271,7 +1275,7 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
   ga.lse = L.lse;
   ga.tgt = a.targets ? L.tgt : nullptr;
   ga.dx = dx;
-  MMF_TRY(loss_rows(a, L, ga, P, *di, st, &launches));
+  MMF_TRY(loss_rows(a, L, ga, nullptr, P, *di, st, &launches));
   P.tgt = ga.tgt;
   P.lse = L.lse;
   P.c = L.c;
@@ -1304,8 +1308,8 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
     else loss_launch<hl::kGrad, true>(P, *di, st);
     if (!a.targets) {
       launch_k(hl::teacher_grad_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
-               a.teacher, (const int32_t*)L.live, (const int32_t*)L.rowmap, s_top, (const float*)L.c,
-               (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.pg);
+               (const int2*)L.top, (const float*)L.q, a.teacher.k, a.teacher.inv_tau, (const int32_t*)L.live,
+               (const int32_t*)L.rowmap, s_top, (const float*)L.c, (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.pg);
       ++launches;
     }
     if (L.pg == 1) loss_launch<hl::kProducts, false>(P, *di, st);
@@ -1450,7 +1454,7 @@ size_t mmf_workspace_bytes(mmf_op op, int64_t m, int32_t d, int32_t inner, int32
     case MMF_OP_HEAD_LOSS:
     case MMF_OP_HEAD_LOSS_BWD:
       return d > 0 && inner > 0 ? loss_plan(m, d, inner, (n_layers & 1) != 0, (n_layers & 2) != 0,
-                                            op == MMF_OP_HEAD_LOSS_BWD, nullptr).bytes : 0;
+                                            op == MMF_OP_HEAD_LOSS_BWD, n_layers >> 2, nullptr).bytes : 0;
     case MMF_OP_BITLINEAR_BWD:
       return d > 0 && inner > 0 ? lin_bwd_plan(m, d, inner).bytes : 0;
     case MMF_OP_DECODE:

@@ -93,7 +93,7 @@ def test_distill_arguments_on_host(L):
                    (11, float("nan")), (11, float("inf"))):
         assert f(*[bad if j == i else a for j, a in enumerate(good)]) == INVALID, (i, bad)
     assert b"distill" in L.mmf_last_error()
-    need = L.mmf_workspace_bytes(mmf.MMF_OP_HEAD_LOSS, 4, 64, 100, 0)
+    need = L.mmf_workspace_bytes(mmf.MMF_OP_HEAD_LOSS, 4, 64, 100, 4 * 8)
     assert f(*good[:15], 256, need - 1, None) == WORKSPACE
     # mmf_lm_head_distill_backward(x, x_dtype, m, d, table, table_dtype, vocab, t_ids, t_logits, t_dtype, top_k,
     #                              temperature, lse, s_top, dloss, dx, dtable, ws, ws_bytes, stream)
@@ -103,7 +103,7 @@ def test_distill_arguments_on_host(L):
         assert b(*[None if j == i else a for j, a in enumerate(good)]) == INVALID, i
     for i, bad in ((10, 0), (10, 257), (11, 0.0), (11, float("nan")), (15, 24), (16, 24)):
         assert b(*[bad if j == i else a for j, a in enumerate(good)]) == INVALID, (i, bad)
-    need = L.mmf_workspace_bytes(mmf.MMF_OP_HEAD_LOSS_BWD, 4, 64, 100, 0)
+    need = L.mmf_workspace_bytes(mmf.MMF_OP_HEAD_LOSS_BWD, 4, 64, 100, 4 * 8)
     assert b(*good[:17], 256, need - 1, None) == WORKSPACE
     assert b(*good[:15], None, None, None, 0, None) == OK
 
@@ -169,12 +169,12 @@ def test_loss_marshalling(fake):  # noqa: F811
     assert a[:7] == (x.data_ptr(), F32, m, d, t.data_ptr(), BF16, v)
     assert a[7:12] == (ids.data_ptr(), tl.data_ptr(), F32, k, 2.0)
     assert a[12:15] == (loss.data_ptr(), lse.data_ptr(), s.data_ptr()) and tuple(s.shape) == (m, k)
-    _ws_ok(a[15], a[16], mmf.MMF_OP_HEAD_LOSS, m, d, v, 1)
+    _ws_ok(a[15], a[16], mmf.MMF_OP_HEAD_LOSS, m, d, v, 1 + 4 * k)
     dx, dt = mmf.lm_head_distill_backward(x, t, ids, tl, lse, s, dl, temperature=2.0)
     a = fake.last("mmf_lm_head_distill_backward")
     assert a[7:12] == (ids.data_ptr(), tl.data_ptr(), F32, k, 2.0)
     assert a[12:17] == (lse.data_ptr(), s.data_ptr(), dl.data_ptr(), dx.data_ptr(), dt.data_ptr())
-    _ws_ok(a[17], a[18], mmf.MMF_OP_HEAD_LOSS_BWD, m, d, v, 1)
+    _ws_ok(a[17], a[18], mmf.MMF_OP_HEAD_LOSS_BWD, m, d, v, 1 + 4 * k)
 
 
 def test_wrappers_refuse_mismatched_arguments(fake):  # noqa: F811
