@@ -120,6 +120,14 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// Programmatic dependent launch: the next kernel's blocks may start (their set-up overlaps this
+// kernel's end), and nothing an earlier kernel wrote is read, and nothing written, before the wait.
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependent() {
+  let_dependents_start();
+  dependency_wait();
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -216,63 +224,84 @@ struct Tile {
   int split;
 };
 
-__host__ __device__ __forceinline__ int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return a / b + (a % b != 0); }
+
+// What all tiles of a launch share, worked out once per thread.
+struct Geo {
+  int tiles;
+  int nt;                  // column tiles
+  int mt;                  // row tiles (kStats, kGrad)
+  int kb_d;                // k-blocks of d
+  int per_dt, per_dx, end_dt;  // kProducts: tiles per split, tiles of dT
+  int kb_dt, len_dt, kb_dx, len_dx;  // k-blocks, k-blocks per split
+};
 
 template <int MODE>
-__device__ __forceinline__ int tile_count(const Params& P, int live) {
-  if (MODE != kProducts) return cdiv(live, BM) * cdiv(P.vn, BN);
-  return P.dt_split * cdiv(P.vn, BM) * cdiv(P.d, BN) + P.dx_split * cdiv(live, BM) * cdiv(P.d, BN);
+__device__ __forceinline__ Geo geometry(const Params& P, int live) {
+  Geo G = {};
+  if (MODE != kProducts) {
+    G.mt = cdiv(live, BM);
+    G.nt = cdiv(P.vn, BN);
+    G.kb_d = cdiv(P.d, BK);
+    G.tiles = G.mt * G.nt;
+  } else {
+    G.nt = cdiv(P.d, BN);
+    G.per_dt = cdiv(P.vn, BM) * G.nt;
+    G.per_dx = cdiv(live, BM) * G.nt;
+    G.end_dt = P.dt_split * G.per_dt;
+    G.tiles = G.end_dt + P.dx_split * G.per_dx;
+    G.kb_dt = cdiv(live, BK);
+    G.kb_dx = cdiv(P.vn, BK);
+    G.len_dt = P.dt_split > 1 ? cdiv(G.kb_dt, P.dt_split) : G.kb_dt;
+    G.len_dx = P.dx_split > 1 ? cdiv(G.kb_dx, P.dx_split) : G.kb_dx;
+  }
+  return G;
 }
 
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const Params& P, int live, int t) {
+__device__ __forceinline__ Tile tile_at(const Params& P, const Geo& G, int t) {
   Tile T;
   T.kind = 0;
   T.split = 0;
   if (MODE != kProducts) {
-    // groups of row tiles, columns slow inside a group: the pairs of one wave share a few row tiles
-    // and a few table tiles, which the L2 then serves
-    constexpr int G = 8;
-    const int mt = cdiv(live, BM), nt = cdiv(P.vn, BN);
-    const int grp = t / (G * nt), rem = t - grp * (G * nt);
-    const int gm = mt - grp * G < G ? mt - grp * G : G;
-    T.row = (grp * G + rem % gm) * BM;
-    T.col = (rem / gm) * BN;
+    // groups of eight row tiles, columns slow inside a group: the pairs of one wave share a few row
+    // tiles and a few table tiles, which the L2 then serves
+    constexpr int R = 8;
+    const int grp = t / (R * G.nt), rem = t - grp * (R * G.nt);
+    const int gm = G.mt - grp * R < R ? G.mt - grp * R : R;
+    const int c = gm == R ? rem / R : rem / gm;
+    T.row = (grp * R + rem - c * gm) * BM;
+    T.col = c * BN;
     T.kb0 = 0;
-    T.nkb = cdiv(P.d, BK);
+    T.nkb = G.kb_d;
     T.nprod = P.fwd.n;
     return T;
   }
-  const int nt = cdiv(P.d, BN);
-  const int per_dt = cdiv(P.vn, BM) * nt, per_dx = cdiv(live, BM) * nt;
-  int kb, splits, rem;
-  if (t < P.dt_split * per_dt) {
-    T.split = t / per_dt;
-    rem = t - T.split * per_dt;
-    kb = cdiv(live, BK);
-    splits = P.dt_split;
+  int kb, len, rem;
+  if (t < G.end_dt) {
+    T.split = P.dt_split > 1 ? t / G.per_dt : 0;
+    rem = t - T.split * G.per_dt;
+    kb = G.kb_dt;
+    len = G.len_dt;
     T.nprod = P.dtp.n;
   } else {
-    t -= P.dt_split * per_dt;
+    t -= G.end_dt;
     T.kind = 1;
-    T.split = t / per_dx;
-    rem = t - T.split * per_dx;
-    kb = cdiv(P.vn, BK);
-    splits = P.dx_split;
+    T.split = P.dx_split > 1 ? t / G.per_dx : 0;
+    rem = t - T.split * G.per_dx;
+    kb = G.kb_dx;
+    len = G.len_dx;
     T.nprod = P.dxp.n;
   }
-  T.row = (rem / nt) * BM;
-  T.col = (rem % nt) * BN;
-  const int per = cdiv(kb, splits);
-  T.kb0 = T.split * per;
-  T.nkb = kb - T.kb0 < per ? kb - T.kb0 : per;
+  const int m = rem / G.nt;
+  T.row = m * BM;
+  T.col = (rem - m * G.nt) * BN;
+  T.kb0 = T.split * len;
+  T.nkb = kb - T.kb0 < len ? kb - T.kb0 : len;
   if (T.nkb < 0) T.nkb = 0;
   return T;
 }
 
-// ---------------------------------------------------------------------------------------------
-// the product kernel
-// ---------------------------------------------------------------------------------------------
 // accumulators (segments of K) of a tile
 template <bool FLUSH>
 __device__ __forceinline__ int tile_segments(const Tile& T) {
@@ -298,6 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t limit = P.wait_limit_us;
   const uint32_t rank = cluster_rank();
+  let_dependents_start();
   const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);  // this pair's tiles
 
   if (threadIdx.x == 0) {
@@ -324,15 +354,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   cluster_sync();  // both CTAs' barriers and tensor memory are set up
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  dependency_wait();
   const int live = *P.live;
-  const int tiles = tile_count<MODE>(P, live);
+  const Geo G = geometry<MODE>(P, live);
+  const int tiles = G.tiles;
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += stride) {
-        const Tile T = tile_at<MODE>(P, live, t);
+        const Tile T = tile_at<MODE>(P, G, t);
         const Prods& pr = MODE != kProducts ? P.fwd : T.kind ? P.dxp : P.dtp;
         for (int p = 0; ok && p < T.nprod; ++p) {
           const int pa = pr.a[p], pb = pr.b[p];
@@ -388,15 +420,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += stride) {
-        const Tile T = tile_at<MODE>(P, live, t);
+        const Tile T = tile_at<MODE>(P, G, t);
         const bool a_mn = MODE == kProducts && T.kind == 0, b_mn = MODE == kProducts;
         const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const int total = T.nprod * T.nkb, segs = tile_segments<FLUSH>(T);
-        for (int g = 0; ok && g < segs; ++g, ++n) {
+        for (int seg = 0; ok && seg < segs; ++seg, ++n) {
           const uint32_t buf = n & 1u, acc = tmem + buf * BN;
           if (!mbar_wait_bounded(&accempty[buf], ((n >> 1) & 1u) ^ 1u, limit, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const int its = !FLUSH ? total : total - g * FLUSH_KB < FLUSH_KB ? total - g * FLUSH_KB : FLUSH_KB;
+          const int its = !FLUSH ? total : total - seg * FLUSH_KB < FLUSH_KB ? total - seg * FLUSH_KB : FLUSH_KB;
           for (int i = 0; i < its; ++i, ++it) {
             const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
             if (!mbar_wait_bounded(&full[s], ph, limit, abort_flag)) { ok = false; break; }
@@ -426,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
     uint32_t n = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += stride) {
-      const Tile T = tile_at<MODE>(P, live, t);
+      const Tile T = tile_at<MODE>(P, G, t);
       const int row0 = T.row + CM * (int)rank + quarter * 32, row = row0 + lane;
       const int col0 = T.col + half * (BN / 2);
       const bool zero = T.nprod * T.nkb == 0;  // no k-blocks: the accumulator was never written
@@ -652,6 +684,7 @@ constexpr int kScanThreads = 1024;
 // inside a warp and a scan over the 32 warps' counts.
 __global__ void __launch_bounds__(kScanThreads) live_rows_kernel(const Rows R, int32_t* __restrict__ rowmap,
                                                                  int32_t* __restrict__ live) {
+  dependent();
   __shared__ int32_t count[2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int base = 0, turn = 0;
@@ -763,6 +796,7 @@ __device__ __forceinline__ void zero_outputs(const GatherArgs& a, int64_t r, int
 // 256 past the live rows, and zeroes the outputs of row i when it is not live itself.
 template <mmf_dtype XT>
 __global__ void __launch_bounds__(kRowThreads) gather_rows_kernel(const GatherArgs a) {
+  dependent();
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   const int live = *a.live;
@@ -779,6 +813,7 @@ constexpr int kOneLaunchRows = 4096;
 template <mmf_dtype XT>
 __global__ void __launch_bounds__(kRowThreads) place_rows_kernel(const GatherArgs a, int32_t* __restrict__ rowmap,
                                                                  int32_t* __restrict__ live_out) {
+  dependent();
   __shared__ int32_t counts[2][kRowThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r0 = blockIdx.x * (kRowThreads / 32);
@@ -821,6 +856,7 @@ __global__ void __launch_bounds__(kRowThreads) place_rows_kernel(const GatherArg
 // float32 table -> three bf16 planes [3][count], 8 values a thread.
 __global__ void __launch_bounds__(kRowThreads) split_table_kernel(const float* __restrict__ t, int64_t count,
                                                                   __nv_bfloat16* __restrict__ out) {
+  dependent();
   const int64_t n8 = count >> 3;
   for (int64_t e = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; e < n8; e += (int64_t)gridDim.x * kRowThreads) {
     const float4 u = reinterpret_cast<const float4*>(t)[2 * e], w = reinterpret_cast<const float4*>(t)[2 * e + 1];
@@ -853,6 +889,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_stats_kernel(const float2* 
                                                                   const int32_t* __restrict__ rowmap,
                                                                   const float* __restrict__ st, float inv_tau,
                                                                   float* loss, float* lse_out) {
+  dependent();
   __shared__ float2 red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int live = *live_p;
@@ -896,6 +933,7 @@ __global__ void __launch_bounds__(kRowThreads) join_planes_kernel(const float* _
                                                                   int64_t plane_rows, int d,
                                                                   const int32_t* __restrict__ count_p, int64_t count_h,
                                                                   const int32_t* __restrict__ rowmap, void* out) {
+  dependent();
   const int nck = d >> 3;
   const int64_t rows = count_p ? *count_p : count_h;
   const int64_t total = rows * nck;
@@ -974,6 +1012,7 @@ __global__ void __launch_bounds__(kTeacherRows * 32) teacher_rows_kernel(const T
                                                                          uint16_t* __restrict__ start,
                                                                          float* __restrict__ s_top,
                                                                          float* __restrict__ q) {
+  dependent();
   __shared__ __align__(16) int32_t ids[kTeacherRows][MAX_TOP];
   __shared__ uint16_t turn[kTeacherTiles][kTeacherRows + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1054,6 +1093,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_loss_kernel(const Teacher
                                                                    const uint8_t* __restrict__ flags,
                                                                    const float* __restrict__ lse,
                                                                    const float* __restrict__ s_top, float* loss) {
+  dependent();
   const int lane = threadIdx.x & 31;
   const int64_t r = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (r >= m || !flags[r]) return;  // the gather has zeroed the row's loss
@@ -1085,6 +1125,7 @@ __global__ void __launch_bounds__(kRowThreads) teacher_grad_kernel(const int2* _
                                                                    const float* __restrict__ lse_p, int v0, int vn,
                                                                    __nv_bfloat16* g, int64_t m_pad, int64_t ldg,
                                                                    int planes) {
+  dependent();
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
   if (i >= *live_p) return;

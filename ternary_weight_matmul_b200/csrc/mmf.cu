@@ -280,6 +280,26 @@ void launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaSt
   cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// The same as a programmatic dependent launch: the kernel may start while the one before it on the
+// stream ends, and itself waits for that one's completion (griddepcontrol.wait) before it reads or
+// writes anything.
+template <typename... KArgs, typename... Args>
+void launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchAttribute attr;
+  memset(&attr, 0, sizeof(attr));
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 mmf_status check_launch(const char* what) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MMF_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
@@ -1032,6 +1052,8 @@ int32_t loss_splits(int64_t tiles, int64_t kb) {
   return best;
 }
 
+inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 struct LossPlan {
   int64_t m_pad;
   int32_t px, pt, pg;       // bf16 planes of x, the table and g
@@ -1082,7 +1104,7 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   if (tf32) L.tp = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pt * vocab * d * 2));
   L.tgt = reinterpret_cast<int32_t*>(take(M * 4));
   if (!backward) {
-    L.parts = 2 * hl::cdiv(vocab, hl::BN);
+    L.parts = (int32_t)(2 * cdiv64(vocab, hl::BN));
     L.part = reinterpret_cast<float2*>(take((size_t)L.parts * M * sizeof(float2)));
     L.st = reinterpret_cast<float*>(take(M * 4));
     if (top_k > 0) L.top_start = reinterpret_cast<uint16_t*>(take((size_t)L.parts * M * sizeof(uint16_t)));
@@ -1099,9 +1121,9 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   L.piece = (v256 / 256 + L.pieces - 1) / L.pieces * 256;  // even pieces
   L.pieces = (int32_t)((vocab + L.piece - 1) / L.piece);
   L.ldg = L.piece;
-  const int64_t nt = hl::cdiv(d, hl::BN);
+  const int64_t nt = cdiv64(d, hl::BN);
   L.dx_split = loss_splits(L.m_pad / hl::BM * nt, L.piece / hl::BK);
-  L.dt_split = loss_splits(hl::cdiv(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
+  L.dt_split = loss_splits(cdiv64(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
   L.g = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pg * M * L.ldg * 2));
   L.dxp = reinterpret_cast<float*>(take((size_t)L.pieces * L.dx_split * M * d * 4));
   if (L.dt_split > 1) L.dtp = reinterpret_cast<float*>(take((size_t)L.dt_split * vocab * d * 4));
@@ -1164,7 +1186,7 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   R.vocab = a.vocab;
   R.m = (int32_t)a.m;
   if (!a.targets) {
-    launch_k(hl::teacher_rows_kernel, dim3((unsigned)(L.m_pad / hl::kTeacherRows)), dim3(hl::kTeacherRows * 32), 0, st,
+    launch_after(hl::teacher_rows_kernel, dim3((unsigned)(L.m_pad / hl::kTeacherRows)), dim3(hl::kTeacherRows * 32), 0, st,
              a.teacher, a.m, L.m_pad, L.parts, L.flags, L.top, L.top_start, s_top, L.q);
     ++*launches;
   }
@@ -1177,20 +1199,20 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   ga.xg = L.xg;
   const dim3 grid(row_ctas), block(hl::kRowThreads);
   if (a.m <= hl::kOneLaunchRows) {
-    if (a.xdt == MMF_F32) launch_k(hl::place_rows_kernel<MMF_F32>, grid, block, 0, st, ga, L.rowmap, L.live);
-    else launch_k(hl::place_rows_kernel<MMF_BF16>, grid, block, 0, st, ga, L.rowmap, L.live);
+    if (a.xdt == MMF_F32) launch_after(hl::place_rows_kernel<MMF_F32>, grid, block, 0, st, ga, L.rowmap, L.live);
+    else launch_after(hl::place_rows_kernel<MMF_BF16>, grid, block, 0, st, ga, L.rowmap, L.live);
     ++*launches;
   } else {
-    launch_k(hl::live_rows_kernel, dim3(1), dim3(hl::kScanThreads), 0, st, R, L.rowmap, L.live);
-    if (a.xdt == MMF_F32) launch_k(hl::gather_rows_kernel<MMF_F32>, grid, block, 0, st, ga);
-    else launch_k(hl::gather_rows_kernel<MMF_BF16>, grid, block, 0, st, ga);
+    launch_after(hl::live_rows_kernel, dim3(1), dim3(hl::kScanThreads), 0, st, R, L.rowmap, L.live);
+    if (a.xdt == MMF_F32) launch_after(hl::gather_rows_kernel<MMF_F32>, grid, block, 0, st, ga);
+    else launch_after(hl::gather_rows_kernel<MMF_BF16>, grid, block, 0, st, ga);
     *launches += 2;
   }
   const void* table = a.table;
   if (a.tdt == MMF_F32) {
     const int64_t count = (int64_t)a.vocab * a.d;
     const unsigned ctas = (unsigned)std::min<int64_t>((count / 8 + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di.sms * 16);
-    launch_k(hl::split_table_kernel, dim3(ctas), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
+    launch_after(hl::split_table_kernel, dim3(ctas), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
              count, L.tp);
     ++*launches;
     table = L.tp;
@@ -1211,7 +1233,7 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
 
 template <int MODE, bool FLUSH>
 void loss_launch(const hl::Params& P, const DevInfo& di, cudaStream_t st) {
-  launch_k(hl::head_loss_kernel<MODE, FLUSH>, dim3((unsigned)di.sms & ~1u), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
+  launch_after(hl::head_loss_kernel<MODE, FLUSH>, dim3((unsigned)di.sms & ~1u), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
 }
 
 mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top, void* ws, size_t ws_bytes,
@@ -1241,12 +1263,12 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
   P.s_top = s_top;
   P.top_k = a.teacher.k;
   loss_launch<hl::kStats, true>(P, *di, st);
-  launch_k(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
+  launch_after(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
            L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
            1.0f / a.tau, loss, lse);
   launches += 2;
   if (!a.targets) {
-    launch_k(hl::distill_loss_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
+    launch_after(hl::distill_loss_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
              a.teacher, a.m, (const uint8_t*)L.flags, (const float*)lse, (const float*)s_top, loss);
     ++launches;
   }
@@ -1307,7 +1329,7 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
     if (L.pg == 1) loss_launch<hl::kGrad, false>(P, *di, st);
     else loss_launch<hl::kGrad, true>(P, *di, st);
     if (!a.targets) {
-      launch_k(hl::teacher_grad_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
+      launch_after(hl::teacher_grad_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
                (const int2*)L.top, (const float*)L.q, a.teacher.k, a.teacher.inv_tau, (const int32_t*)L.live,
                (const int32_t*)L.rowmap, s_top, (const float*)L.c, (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.pg);
       ++launches;
@@ -1320,9 +1342,9 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
                         mmf_dtype odt, void* out) {
     const unsigned ctas = (unsigned)std::min<int64_t>((rows * (a.d / 8) + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di->sms * 16);
     if (odt == MMF_F32)
-      launch_k(hl::join_planes_kernel<MMF_F32>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
+      launch_after(hl::join_planes_kernel<MMF_F32>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
     else
-      launch_k(hl::join_planes_kernel<MMF_BF16>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
+      launch_after(hl::join_planes_kernel<MMF_BF16>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
     ++launches;
   };
   if (dx) join(L.dxp, L.pieces * L.dx_split, L.m_pad, L.live, L.rowmap, a.xdt, dx);
