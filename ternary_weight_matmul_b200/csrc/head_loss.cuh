@@ -37,16 +37,17 @@ constexpr int BM = 2 * CM;     // rows of D per tile (MMA M, over the pair)
 constexpr int BN = 256;        // columns of D per tile (MMA N)
 constexpr int BK = 64;         // bf16 per k-block: one 128-byte swizzle atom
 constexpr int UK = 16;         // K per kind::f16 instruction
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int FLUSH_KB = 8;    // k-blocks per accumulator where pieces are added in registers
 constexpr int BOX_BYTES = 64 * BK * 2;  // every TMA load box: 64 x 64 bf16, 8 KB
 constexpr int A_BOXES = CM / 64, B_BOXES = BN / 2 / 64;  // per CTA
 constexpr int STAGE_BYTES = (A_BOXES + B_BOXES) * BOX_BYTES;
 constexpr int EPI_WARPS = 8;   // two per tensor-memory lane quarter, each half of the columns
 constexpr int THREADS = (4 + EPI_WARPS) * 32;
-constexpr int OUT_BYTES = 4096;  // staging per epilogue warp: 32 rows x 128 bytes
+constexpr int OUT_BYTES = 4096;  // a staging buffer of an epilogue warp: 32 rows x 128 bytes
+constexpr int OUT_BUFS = 2;      // ... of which one is filled while the other one is being stored
 constexpr int NUM_BARS = 2 * STAGES + 5;
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES + NUM_BARS * 8 + 16;
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_WARPS * OUT_BUFS * OUT_BYTES + NUM_BARS * 8 + 16;
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int PLANES = 3;      // bf16 planes of a float32 operand
 constexpr int MAX_PRODS = 6;
@@ -114,7 +115,9 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all stores but the latest N have read their shared memory
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -314,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + STAGES * STAGE_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI_WARPS * OUT_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI_WARPS * OUT_BUFS * OUT_BYTES);
   // full and accempty count in the pair's first CTA (both CTAs' copies and epilogue warps); empty,
   // accfull and drain are each CTA's own, reached by the MMA thread's multicast commits
   uint64_t* full = bars;                     // TMA -> MMA           (count 1 + both CTAs' bytes)
@@ -453,8 +456,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t stg = smem_u32(staging + (warp - 4) * OUT_BYTES);
-    const uint32_t swz = (uint32_t)(lane & 7) << 4, stg_row = stg + lane * 128;
+    const uint32_t stg0 = smem_u32(staging + (warp - 4) * OUT_BUFS * OUT_BYTES);
+    const uint32_t swz = (uint32_t)(lane & 7) << 4;
+    uint32_t stg = stg0, stg_row = stg0 + lane * 128;  // the buffer being filled
+    const auto next_buffer = [&] {
+      if (OUT_BUFS > 1) stg = stg == stg0 ? stg0 + OUT_BYTES : stg0;
+      stg_row = stg + lane * 128;
+    };
     uint32_t n = 0;
     bool ok = true;
     for (int t = first; ok && t < tiles; t += stride) {
@@ -581,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           }
 #pragma unroll
           for (int p = 0; p < (FLUSH ? PLANES : 1); ++p) {
-            if (lane == 0) bulk_wait_read();
+            if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -602,6 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
               tma_store_3d(&P.g_out, stg, col0 + c0, row0, p);
               bulk_commit();
             }
+            next_buffer();
           }
         }
       } else {
@@ -617,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           if (!FLUSH) cols32(c0, v);
           const int h = f32 ? 0 : (c0 >> 5) & 1;  // bf16: two groups of 32 columns fill a 128-byte row
           if (h == 0) {
-            if (lane == 0) bulk_wait_read();
+            if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
             __syncwarp();
           }
           if (f32) {
@@ -641,6 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
               tma_store_3d(map, stg, col0 + c0 - 32 * h, out_row, plane);
               bulk_commit();
             }
+            next_buffer();
           }
         }
       }
