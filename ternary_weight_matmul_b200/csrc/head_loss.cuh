@@ -16,9 +16,19 @@
 // 128 x 256 of D, so that a k-block costs 32 KB of L2 reads per CTA; with single CTAs and 128 x 256
 // tiles it is 48 KB, and those reads (13.5 TB/s) held the kernel at 1150 TFLOP/s. Per CTA a TMA
 // producer thread and eight epilogue warps, one MMA thread in the pair's first CTA, persistent over
-// tiles, two accumulators in tensor memory so that a tile's epilogue runs under the next tile's MMAs. Operands are bf16; a float32 operand enters as three
-// bf16 planes that add up to it exactly (8 + 8 + 8 significant bits, by truncation), and a product
-// of float32 accuracy runs over the plane pairs (i, j) with i + j <= 2, smallest terms first.
+// tiles, two accumulators in tensor memory so that a tile's epilogue runs under the next tile's MMAs.
+//
+// Operands of a bf16 table are bf16; float32 rows beside it enter as three bf16 planes that add up to
+// them exactly (8 + 8 + 8 significant bits, by truncation), and a product of float32 accuracy runs over
+// the plane pairs (i, j) with i + j <= 2, smallest terms first.
+//
+// With a float32 table everything is fp16 in two planes instead, hi = fp16(v 2^k), lo = fp16(v 2^k -
+// hi): 11 + 11 bits rounded to nearest, within 2^-22 of v, so three pairs (i + j <= 1; what they drop is
+// 2^-22 too) do what six do in bf16. The power of two keeps fp16's range: one per row for x (taken out
+// in the epilogue), one for the table, one for c x (c = dloss / tau), which is the rows' side of dT, and
+// 2^15 for g / c = p - teacher, which lies in [-1, 1]. Values below 2^-17 of such a maximum lose bits
+// one by one down to steps of 2^-39 of it: less than float32's rounding of the sums they enter, though
+// not of a single p far below 2^-17.
 //
 // The tensor cores' float32 accumulator cuts bits off at every step of K = 16, towards zero: a bias of
 // about half an ulp of the running sum per step, 1.3e-6 of logits of size 2 at d = 1024 and 3.8e-6 at
@@ -26,6 +36,8 @@
 // statistics, and every gradient with a float32 operand) the kernel therefore starts a new accumulator
 // every FLUSH_KB k-blocks and the epilogue adds the pieces in registers, rounding to nearest.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 
@@ -64,10 +76,11 @@ struct Prods {
 };
 
 struct Params {
-  CUtensorMap x;    // live rows, planes   [px][m_pad][d] bf16, box 64 x 64 (all loads)
-  CUtensorMap t;    // table, planes       [pt][vocab][d] bf16
-  CUtensorMap g;    // the piece's g       [pg][m_pad][ldg] bf16, inner extent = piece columns; one plane
-                    // rounded to nearest, or with FLUSH three that split it exactly
+  CUtensorMap x;    // live rows, planes   [px][m_pad][d], 16 bits, box 64 x 64 (all loads); kProducts with
+                    // a float32 table: c x
+  CUtensorMap t;    // table, planes       [pt][vocab][d]
+  CUtensorMap g;    // the piece's g       [pg][m_pad][ldg], inner extent = piece columns; one plane
+                    // rounded to nearest, three that split it exactly, or (fp16) two of g / c
   CUtensorMap g_out;   // the same array, box 64 x 32 (stores)
   CUtensorMap dx_out;  // float32 partials [planes][m_pad][d], box 32 x 32
   CUtensorMap dt_out;  // dtable's rows of the piece (its dtype), or float32 partials [planes][vocab][d]
@@ -91,6 +104,10 @@ struct Params {
   int32_t dx_split, dx_plane0;  // K splits of dx in this launch (0: no dx) and its first partial plane
   int32_t dt_split;             // K splits of dT (0: no dT)
   int32_t dt_f32;               // dt_out holds float32
+  // float32 tables (fp16 planes): the powers of two to take out, else nullptr
+  const float* x_unit;          // [m_pad] of each row of x
+  const float* t_unit;          // of the table
+  const float* dt_unit;         // of c x
   int32_t dt_row0;              // first row of dt_out this launch writes
   uint32_t wait_limit_us;
 };
@@ -206,6 +223,28 @@ __device__ __forceinline__ void split3(float v, float& p0, float& p1, float& p2)
   p0 = peel(v);
   p1 = peel(v);
   p2 = peel(v);
+}
+// v 2^k as two fp16 planes; v leaves with the rest after the first. An infinity or NaN stays whole.
+constexpr float kGradUnit = 32768.0f;  // g / c as fp16: |g / c| <= 1
+__device__ __forceinline__ float peel_half(float& v) {
+  const float h = __half2float(__float2half_rn(v));
+  v = (__float_as_uint(h) & 0x7f800000u) == 0x7f800000u ? 0.0f : v - h;
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 2^k that brings `most`, the largest finite magnitude, to [2^14, 2^15); within what a float32 holds.
+__device__ __forceinline__ float unit_up(float most) {
+  int e = (int)(__float_as_uint(most) >> 23) - 127;  // floor(log2); -127 for zero and subnormals
+  int k = 14 - e;
+  k = k < -110 ? -110 : k > 110 ? 110 : k;
+  return most > 0.0f ? __uint_as_float((uint32_t)(127 + k) << 23) : 1.0f;
+}
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a <= 3.402823466e38f ? a : 0.0f;  // infinities and NaN do not count
 }
 __device__ __forceinline__ uint32_t pack_bf16_rn(float a, float b) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -416,10 +455,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0 && rank == 0) {
-      // kind::f16: D float32 (bits 4-5 = 1), A and B bf16 (bits 7-9, 10-12 = 1), MN-major A / B at
+      // kind::f16: D float32 (bits 4-5 = 1), A and B bf16 or fp16 (bits 7-9, 10-12), MN-major A / B at
       // bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28
-      constexpr uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
-                                  ((uint32_t)(BM >> 4) << 24);
+      const uint32_t fmt = P.t_unit ? 0u : 1u;  // fp16 : bf16
+      const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(BN >> 3) << 17) |
+                              ((uint32_t)(BM >> 4) << 24);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += stride) {
@@ -500,6 +540,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
         for (int e = 0; e < (FLUSH ? BN / 2 : 1); ++e) sum[e] = 0.0f;
       }
+      if (FLUSH && P.t_unit && (MODE != kProducts || T.kind == 0)) {
+        // dx's units go where its partials are added
+        const float u = MODE == kProducts ? *P.dt_unit * (1.0f / kGradUnit) : (row < live ? P.x_unit[row] : 0.0f);
+        const float ut = MODE == kProducts ? 1.0f : *P.t_unit;
+#pragma unroll
+        for (int e = 0; e < (FLUSH ? BN / 2 : 1); ++e) sum[e] = sum[e] * u * ut;
+      }
       // columns [c0, c0 + N) of D into v (with FLUSH they are in `sum` already)
       const auto cols32 = [&](int c0, float* v) {
         uint32_t w[32];
@@ -563,7 +610,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         }
       } else if (MODE == kGrad) {
         // pad rows have c = lse = 0: zeros, which the products over the live rows rely on
-        const float c = P.c[row], lse2 = P.lse[row] * kLog2e;
+        const bool halves = FLUSH && P.t_unit;
+        const float c = !halves ? P.c[row] : row < live ? kGradUnit : 0.0f, lse2 = P.lse[row] * kLog2e;
         const int tgt = P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
         const auto grads = [&](float* gv, int c0, int w) {
 #pragma unroll
@@ -589,6 +637,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           }
 #pragma unroll
           for (int p = 0; p < (FLUSH ? PLANES : 1); ++p) {
+            if (FLUSH && p == 2 && halves) break;
             if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
             __syncwarp();
 #pragma unroll
@@ -600,7 +649,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
                 float& b = gv[8 * j + 2 * q + 1];
                 // keeps the compiler from splitting all values ahead of the stores, into spills
                 asm volatile("" : "+f"(a), "+f"(b));
-                w[q] = FLUSH ? pack_bf16_hi(peel(a), peel(b)) : pack_bf16_rn(a, b);
+                if (!FLUSH) w[q] = pack_bf16_rn(a, b);
+                else if (halves) w[q] = pack_half(peel_half(a), peel_half(b));
+                else w[q] = pack_bf16_hi(peel(a), peel(b));
               }
               st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), w[0], w[1], w[2], w[3]);
             }
@@ -733,7 +784,9 @@ struct GatherArgs {
   const void* x;          // [m][d]
   int32_t d;
   int64_t m_pad;
-  __nv_bfloat16* xg;      // [planes][m_pad][d]
+  __nv_bfloat16* xg;      // [planes][m_pad][d], fp16 with a float32 table
+  float* x_unit;          // fp16: [m_pad] the power of two to take out again, or nullptr
+  float* row_most;        // fp16, backward: [m_pad] largest |c x| of each place
   // backward, per live row (pad rows: 0): c = dloss / tau, lse, target
   const float* dloss;     // [m] or nullptr
   const float* lse_in;    // [m]
@@ -749,31 +802,76 @@ struct GatherArgs {
 
 constexpr int kRowThreads = 256;
 
-// Live row r -> place i (float32 rows as three planes). Whole warp, as the next two.
+__device__ __forceinline__ void store_planes(const GatherArgs& a, int64_t i, int c, const uint32_t (*p)[4], int planes) {
+  for (int j = 0; j < planes; ++j)
+    reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d)[c] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+}
+template <mmf_dtype XT>
+__device__ __forceinline__ void load_row8(const void* x, int64_t at, float (&v)[8]) {
+  if (XT == MMF_F32) {
+    const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + at);
+    const float4 u = s[0], w = s[1];
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(x) + at);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[2 * q] = __uint_as_float(w[q] << 16);
+      v[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+    }
+  }
+}
+// eight values as fp16 planes: two of them, or one (bf16 rows: eight bits fit in eleven)
+template <int N>
+__device__ __forceinline__ void half_planes(float (&v)[8], uint32_t (&p)[PLANES][4]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) p[j][q] = pack_half(peel_half(v[2 * q]), peel_half(v[2 * q + 1]));
+}
+
+// Live row r -> place i (float32 rows as planes; fp16 rows by their own power of two). Whole warp, as
+// the next two.
 template <mmf_dtype XT>
 __device__ __forceinline__ void place_row(const GatherArgs& a, int64_t i, int64_t r, int lane) {
   const int nck = a.d >> 3;
-  for (int c = lane; c < nck; c += 32) {
-    if (XT == MMF_BF16) {
-      reinterpret_cast<uint4*>(a.xg + i * a.d)[c] =
-          reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + r * a.d)[c];
-    } else {
-      const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x) + r * a.d) + 2 * c;
-      const float4 u = s[0], w = s[1];
-      const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-      uint32_t p[PLANES][4];
+  float v[8];
+  uint32_t p[PLANES][4];
+  if (a.x_unit) {
+    float most = 0.0f;
+    for (int c = lane; c < nck; c += 32) {
+      load_row8<XT>(a.x, r * a.d + 8 * c, v);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float a0, a1, a2, b0, b1, b2;
-        split3(v[2 * q], a0, a1, a2);
-        split3(v[2 * q + 1], b0, b1, b2);
-        p[0][q] = pack_bf16_hi(a0, b0);
-        p[1][q] = pack_bf16_hi(a1, b1);
-        p[2][q] = pack_bf16_hi(a2, b2);
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, finite_abs(v[e]));
+    }
+    most = warp_max(most);
+    const float up = unit_up(most);
+    for (int c = lane; c < nck; c += 32) {
+      load_row8<XT>(a.x, r * a.d + 8 * c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= up;
+      half_planes<XT == MMF_F32 ? 2 : 1>(v, p);
+      store_planes(a, i, c, p, XT == MMF_F32 ? 2 : 1);
+    }
+    if (lane == 0) {
+      a.x_unit[i] = 1.0f / up;
+      if (a.row_most) a.row_most[i] = finite_abs(most * a.dloss[r] * a.inv_tau);
+    }
+  } else {
+    for (int c = lane; c < nck; c += 32) {
+      if (XT == MMF_BF16) {
+        reinterpret_cast<uint4*>(a.xg + i * a.d)[c] =
+            reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + r * a.d)[c];
+        continue;
       }
+      load_row8<XT>(a.x, r * a.d + 8 * c, v);
 #pragma unroll
       for (int j = 0; j < PLANES; ++j)
-        reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d)[c] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p[j][q] = pack_bf16_hi(peel(v[2 * q]), peel(v[2 * q + 1]));
+      store_planes(a, i, c, p, PLANES);
     }
   }
   if (lane == 0 && a.c) {
@@ -785,10 +883,11 @@ __device__ __forceinline__ void place_row(const GatherArgs& a, int64_t i, int64_
 // zeros in a place past the live rows
 template <mmf_dtype XT>
 __device__ __forceinline__ void zero_place(const GatherArgs& a, int64_t i, int lane) {
-  for (int j = 0; j < (XT == MMF_F32 ? PLANES : 1); ++j)
+  for (int j = 0; j < (XT == MMF_F32 ? (a.x_unit ? 2 : PLANES) : 1); ++j)
     for (int c = lane; c < a.d >> 3; c += 32)
       reinterpret_cast<uint4*>(a.xg + (j * a.m_pad + i) * a.d)[c] = make_uint4(0u, 0u, 0u, 0u);
   if (lane == 0 && a.c) a.c[i] = a.lse[i] = 0.0f;
+  if (lane == 0 && a.row_most) a.row_most[i] = 0.0f;
   if (lane == 0 && a.tgt) a.tgt[i] = -1;
 }
 // zeros in the outputs of a row that is not live
@@ -863,27 +962,91 @@ __global__ void __launch_bounds__(kRowThreads) place_rows_kernel(const GatherArg
   if (r0 == 0 && threadIdx.x == 0) *live_out = total;
 }
 
-// float32 table -> three bf16 planes [3][count], 8 values a thread.
-__global__ void __launch_bounds__(kRowThreads) split_table_kernel(const float* __restrict__ t, int64_t count,
-                                                                  __nv_bfloat16* __restrict__ out) {
+constexpr int kMostParts = 592;  // four CTAs per SM
+
+__device__ __forceinline__ float reduce_most(float v, float* red) {  // red: 32 floats; all threads get the result
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = threadIdx.x < kRowThreads / 32 ? red[threadIdx.x] : 0.0f;
+  if (threadIdx.x < 32) {
+    v = warp_max(v);
+    if (threadIdx.x == 0) red[0] = v;
+  }
+  __syncthreads();
+  return red[0];
+}
+
+// Largest finite magnitude of a float32 table, one value per CTA.
+__global__ void __launch_bounds__(kRowThreads) table_most_kernel(const float* __restrict__ t, int64_t count,
+                                                                 float* __restrict__ parts) {
+  __shared__ float red[32];
   dependent();
+  const int64_t n4 = count >> 2;
+  float most = 0.0f;
+  for (int64_t e = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; e < n4; e += (int64_t)gridDim.x * kRowThreads) {
+    const float4 u = reinterpret_cast<const float4*>(t)[e];
+    most = fmaxf(most, fmaxf(fmaxf(finite_abs(u.x), finite_abs(u.y)), fmaxf(finite_abs(u.z), finite_abs(u.w))));
+  }
+  most = reduce_most(most, red);
+  if (threadIdx.x == 0) parts[blockIdx.x] = most;
+}
+
+// float32 table -> two fp16 planes [2][count] and the power of two to take out again, 8 values a thread.
+__global__ void __launch_bounds__(kRowThreads) split_table_kernel(const float* __restrict__ t, int64_t count,
+                                                                  const float* __restrict__ parts, int nparts,
+                                                                  __nv_bfloat16* __restrict__ out,
+                                                                  float* __restrict__ unit) {
+  __shared__ float red[32];
+  dependent();
+  float most = 0.0f;
+  for (int i = threadIdx.x; i < nparts; i += kRowThreads) most = fmaxf(most, parts[i]);
+  const float up = unit_up(reduce_most(most, red));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *unit = 1.0f / up;
   const int64_t n8 = count >> 3;
   for (int64_t e = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; e < n8; e += (int64_t)gridDim.x * kRowThreads) {
-    const float4 u = reinterpret_cast<const float4*>(t)[2 * e], w = reinterpret_cast<const float4*>(t)[2 * e + 1];
-    const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+    float v[8];
     uint32_t p[PLANES][4];
+    load_row8<MMF_F32>(t, 8 * e, v);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float a0, a1, a2, b0, b1, b2;
-      split3(v[2 * q], a0, a1, a2);
-      split3(v[2 * q + 1], b0, b1, b2);
-      p[0][q] = pack_bf16_hi(a0, b0);
-      p[1][q] = pack_bf16_hi(a1, b1);
-      p[2][q] = pack_bf16_hi(a2, b2);
-    }
+    for (int i = 0; i < 8; ++i) v[i] *= up;
+    half_planes<2>(v, p);
 #pragma unroll
-    for (int j = 0; j < PLANES; ++j)
+    for (int j = 0; j < 2; ++j)
       reinterpret_cast<uint4*>(out + j * count)[e] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+  }
+}
+
+// c x of the live rows as fp16 planes under one power of two, the rows' side of dT with a float32
+// table; zeros in the places up to the next multiple of 256. One warp per place; every CTA takes the
+// largest |c x| over the places from row_most.
+template <mmf_dtype XT>
+__global__ void __launch_bounds__(kRowThreads) weigh_rows_kernel(const GatherArgs a, __nv_bfloat16* __restrict__ out,
+                                                                 float* __restrict__ unit) {
+  __shared__ float red[32];
+  dependent();
+  const int live = *a.live, lane = threadIdx.x & 31, nck = a.d >> 3;
+  const int64_t places = ((int64_t)live + 255) & ~(int64_t)255;
+  if ((int64_t)blockIdx.x * (kRowThreads / 32) >= places && blockIdx.x > 0) return;  // uniform
+  float most = 0.0f;
+  for (int i = threadIdx.x; i < live; i += kRowThreads) most = fmaxf(most, a.row_most[i]);
+  const float up = unit_up(reduce_most(most, red));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *unit = 1.0f / up;
+  for (int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); i < places;
+       i += (int64_t)gridDim.x * (kRowThreads / 32)) {
+    const float c = i < live ? a.c[i] : 0.0f;
+    const int64_t r = i < live ? a.rowmap[i] : 0;
+    for (int k = lane; k < nck; k += 32) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      uint32_t p[PLANES][4];
+      if (i < live) load_row8<XT>(a.x, r * a.d + 8 * k, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * c * up;
+      half_planes<2>(v, p);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        reinterpret_cast<uint4*>(out + (j * a.m_pad + i) * a.d)[k] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+    }
   }
 }
 
@@ -937,12 +1100,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_stats_kernel(const float2* 
 }
 
 // out[row(i)][:] = sum over planes of part[p][i][:], in plane order; rows i < *count (or count_h),
-// written to rowmap[i] when given. 8 columns a thread.
+// written to rowmap[i] when given, times c_p[i] and dx's fp16 units when given. 8 columns a thread.
 template <mmf_dtype OT>
 __global__ void __launch_bounds__(kRowThreads) join_planes_kernel(const float* __restrict__ part, int planes,
                                                                   int64_t plane_rows, int d,
                                                                   const int32_t* __restrict__ count_p, int64_t count_h,
-                                                                  const int32_t* __restrict__ rowmap, void* out) {
+                                                                  const int32_t* __restrict__ rowmap,
+                                                                  const float* __restrict__ c_p,
+                                                                  const float* __restrict__ unit, void* out) {
   dependent();
   const int nck = d >> 3;
   const int64_t rows = count_p ? *count_p : count_h;
@@ -958,6 +1123,11 @@ __global__ void __launch_bounds__(kRowThreads) join_planes_kernel(const float* _
       v[4] += w.x; v[5] += w.y; v[6] += w.z; v[7] += w.w;
     }
     const int64_t r = rowmap ? rowmap[i] : i;
+    if (c_p) {
+      const float u = *unit * (1.0f / kGradUnit), c = c_p[i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * u * c;
+    }
     if (OT == MMF_F32) {
       float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + r * d) + 2 * c;
       o[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -1146,8 +1316,15 @@ __global__ void __launch_bounds__(kRowThreads) teacher_grad_kernel(const int2* _
     if (e.x < v0 || e.x >= v0 + vn || (p > 0 && top[base + p - 1].x == e.x)) continue;
     float w = q[base + p];
     for (int n = p + 1; n < k && top[base + n].x == e.x; ++n) w += q[base + n];
-    float v = c * (expf(s_top[base + e.y] * inv_tau - L) - w);
+    float v = expf(s_top[base + e.y] * inv_tau - L) - w;
     __nv_bfloat16* o = g + i * ldg + (e.x - v0);
+    if (planes == 2) {  // fp16, without c
+      v *= kGradUnit;
+      for (int pl = 0; pl < 2; ++pl)
+        *reinterpret_cast<__half*>(o + pl * m_pad * ldg) = __float2half_rn(peel_half(v));
+      continue;
+    }
+    v *= c;
     if (planes == 1) *o = __float2bfloat16_rn(v);
     else
       for (int pl = 0; pl < PLANES; ++pl) o[pl * m_pad * ldg] = __float2bfloat16_rn(peel(v));

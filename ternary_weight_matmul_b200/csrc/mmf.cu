@@ -1064,7 +1064,13 @@ struct LossPlan {
   int32_t* rowmap;
   uint8_t* flags;
   __nv_bfloat16* xg;
-  __nv_bfloat16* tp;        // table planes (float32 tables)
+  // float32 tables
+  __nv_bfloat16* tp;        // table planes
+  __nv_bfloat16* xw;        // c x planes
+  float* most;              // largest magnitudes of the table, per CTA
+  float* units;             // powers of two to take out: of the table, of c x
+  float* x_unit;            // ... of each row
+  float* row_most;
   float2* part;
   float* st;
   int2* top;                // distillation: the teacher's entries in order of their ids
@@ -1090,9 +1096,9 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
     return r;
   };
   L.m_pad = (m + 255) / 256 * 256;
-  L.px = xf32 ? hl::PLANES : 1;
-  L.pt = tf32 ? hl::PLANES : 1;
-  L.pg = xf32 || tf32 ? hl::PLANES : 1;
+  L.px = xf32 ? (tf32 ? 2 : hl::PLANES) : 1;
+  L.pt = tf32 ? 2 : 1;
+  L.pg = tf32 ? 2 : xf32 ? hl::PLANES : 1;
   const size_t M = (size_t)L.m_pad;
   L.live = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   L.rowmap = reinterpret_cast<int32_t*>(take(M * 4));
@@ -1101,7 +1107,16 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
     L.top = reinterpret_cast<int2*>(take((size_t)m * top_k * sizeof(int2)));
   }
   L.xg = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.px * M * d * 2));
-  if (tf32) L.tp = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pt * vocab * d * 2));
+  if (tf32) {
+    L.tp = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pt * vocab * d * 2));
+    L.most = reinterpret_cast<float*>(take(hl::kMostParts * sizeof(float)));
+    L.units = reinterpret_cast<float*>(take(2 * sizeof(float)));
+    L.x_unit = reinterpret_cast<float*>(take(M * 4));
+    if (backward) {
+      L.xw = reinterpret_cast<__nv_bfloat16*>(take(2 * M * d * 2));
+      L.row_most = reinterpret_cast<float*>(take(M * 4));
+    }
+  }
   L.tgt = reinterpret_cast<int32_t*>(take(M * 4));
   if (!backward) {
     L.parts = (int32_t)(2 * cdiv64(vocab, hl::BN));
@@ -1197,6 +1212,8 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   ga.d = a.d;
   ga.m_pad = L.m_pad;
   ga.xg = L.xg;
+  ga.x_unit = L.x_unit;
+  ga.row_most = L.row_most;
   const dim3 grid(row_ctas), block(hl::kRowThreads);
   if (a.m <= hl::kOneLaunchRows) {
     if (a.xdt == MMF_F32) launch_after(hl::place_rows_kernel<MMF_F32>, grid, block, 0, st, ga, L.rowmap, L.live);
@@ -1212,10 +1229,22 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   if (a.tdt == MMF_F32) {
     const int64_t count = (int64_t)a.vocab * a.d;
     const unsigned ctas = (unsigned)std::min<int64_t>((count / 8 + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di.sms * 16);
+    const int parts = (int)std::min<unsigned>(ctas, hl::kMostParts);
+    launch_after(hl::table_most_kernel, dim3(parts), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
+                 count, L.most);
     launch_after(hl::split_table_kernel, dim3(ctas), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
-             count, L.tp);
-    ++*launches;
+                 count, (const float*)L.most, parts, L.tp, L.units);
+    *launches += 2;
     table = L.tp;
+    if (L.xw) {
+      const unsigned wctas = (unsigned)std::min<int64_t>(row_ctas, (int64_t)di.sms * 8);
+      if (a.xdt == MMF_F32) launch_after(hl::weigh_rows_kernel<MMF_F32>, dim3(wctas), block, 0, st, ga, L.xw, L.units + 1);
+      else launch_after(hl::weigh_rows_kernel<MMF_BF16>, dim3(wctas), block, 0, st, ga, L.xw, L.units + 1);
+      ++*launches;
+    }
+    P.x_unit = L.x_unit;
+    P.t_unit = L.units;
+    P.dt_unit = L.units + 1;
   }
   MMF_TRY(check_launch("head loss row kernels"));
   const uint64_t row = (uint64_t)a.d * 2;
@@ -1226,7 +1255,7 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   P.vocab = a.vocab;
   P.m_pad = L.m_pad;
   P.scale = hl::kLog2e / a.tau;
-  P.fwd = loss_prods(L.px, L.pt, 2);
+  P.fwd = loss_prods(L.px, L.pt, a.tdt == MMF_F32 ? 1 : 2);
   P.wait_limit_us = g_wait_limit.load();
   return MMF_OK;
 }
@@ -1301,8 +1330,16 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
   P.tgt = ga.tgt;
   P.lse = L.lse;
   P.c = L.c;
-  P.dxp = loss_prods(L.pg, L.pt, L.pg == 1 ? 0 : a.xdt == MMF_F32 ? 2 : 1);
-  P.dtp = loss_prods(L.pg, L.px, L.pg == 1 ? 0 : a.tdt == MMF_F32 ? 2 : 1);
+  // a float32 result takes every pair; a bf16 one of three bf16 planes the pairs above 2^-15, of fp16
+  // planes (2^-12 each) the first alone
+  const bool halves = a.tdt == MMF_F32;
+  P.dxp = loss_prods(L.pg, L.pt, halves ? (a.xdt == MMF_F32 ? 1 : 0) : L.pg == 1 ? 0 : 2);
+  P.dtp = loss_prods(L.pg, halves ? 2 : L.px, halves || L.pg > 1 ? 1 : 0);
+  CUtensorMap weighed;
+  if (halves)
+    MMF_TRY(encode_3d(&weighed, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.xw, a.d, L.m_pad, 2, (uint64_t)a.d * 2,
+                      (uint64_t)L.m_pad * a.d * 2, hl::BK, 64));
+  const CUtensorMap rows = P.x;
   P.dx_split = dx ? L.dx_split : 0;
   P.dt_split = dtable ? L.dt_split : 0;
   const uint64_t f32row = (uint64_t)a.d * 4, trow = (uint64_t)a.d * dsize(a.tdt);
@@ -1334,21 +1371,23 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
                (const int32_t*)L.rowmap, s_top, (const float*)L.c, (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.pg);
       ++launches;
     }
+    if (halves) P.x = weighed;
     if (L.pg == 1) loss_launch<hl::kProducts, false>(P, *di, st);
     else loss_launch<hl::kProducts, true>(P, *di, st);
+    P.x = rows;
     launches += 2;
   }
   const auto join = [&](const float* part, int planes, int64_t rows, const int32_t* count, const int32_t* map,
-                        mmf_dtype odt, void* out) {
+                        mmf_dtype odt, void* out, const float* c, const float* unit) {
     const unsigned ctas = (unsigned)std::min<int64_t>((rows * (a.d / 8) + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di->sms * 16);
     if (odt == MMF_F32)
-      launch_after(hl::join_planes_kernel<MMF_F32>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
+      launch_after(hl::join_planes_kernel<MMF_F32>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, c, unit, out);
     else
-      launch_after(hl::join_planes_kernel<MMF_BF16>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, out);
+      launch_after(hl::join_planes_kernel<MMF_BF16>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, c, unit, out);
     ++launches;
   };
-  if (dx) join(L.dxp, L.pieces * L.dx_split, L.m_pad, L.live, L.rowmap, a.xdt, dx);
-  if (dtable && L.dt_split > 1) join(L.dtp, L.dt_split, a.vocab, nullptr, nullptr, a.tdt, dtable);
+  if (dx) join(L.dxp, L.pieces * L.dx_split, L.m_pad, L.live, L.rowmap, a.xdt, dx, halves ? L.c : nullptr, L.units);
+  if (dtable && L.dt_split > 1) join(L.dtp, L.dt_split, a.vocab, nullptr, nullptr, a.tdt, dtable, nullptr, nullptr);
   g_launches.fetch_add(launches - 1);  // the timing scope counted one launch itself
   return check_launch("head loss backward kernels");
 }

@@ -10,6 +10,11 @@ which may truncate; h(t) = finfo(t).eps / 2 per rounding to t):
         in bf16 (both operands bf16); the teacher's share q is a float32 softmax: 64 u
   dx    e_g |T| + (6 n + 64) u (|g| |T|), n = vocab terms, plus h(dtype) of |dx|; dtable likewise.
   What is below the smallest normal float32 counts as zero: 2^-126 on p, on g and on every product.
+  With a float32 table the operands are pairs of fp16 values under a power of two that brings the
+  largest of them to 2^14 at least: 2^-22 relative (three roundings or dropped terms a product, inside
+  the n u above) and 2^-25 / 2^14 of the largest absolutely (the last fp16 step is 2^-24): of a row of
+  x, of the table, of c x, and of 1 for g / c. A bf16 result takes the leading fp16 values alone: two
+  roundings of 2^-11.
 These worst cases grow with the number of terms; what the kernels do does not: an accumulator takes 16
 steps (of at most u of its sum each) before the pieces are added rounding to nearest. So results are also
 held to 16 u of their norm, and gradients, through p's relative error being s's absolute one, to
@@ -28,6 +33,7 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 U = 2.0 ** -23
 TINY = 2.0 ** -126
+STEP16 = 2.0 ** -39
 F32, BF16 = torch.float32, torch.bfloat16
 ORDER6 = 6
 
@@ -81,8 +87,13 @@ class Ref:
         self.x = torch.where(live[:, None], self.x, 0.0)
         self.q = q
         self.s = self.x @ self.t.T
+        self.halves = t.dtype == F32
         self.lse = torch.logsumexp(self.s / tau, 1)
         self.e_s = ORDER6 * x.shape[1] * U * (self.x.abs() @ self.t.abs().T) / tau + 4 * U * self.s.abs() / tau
+        if self.halves:
+            ax, at = self.x.abs(), self.t.abs()
+            self.e_s = self.e_s + STEP16 * (ax.sum(1, keepdim=True) * at.max() + ax.max(1, keepdim=True).values
+                                            * at.sum(1)[None]) / tau
         self.e_lse = self.e_s.max(1).values + 64 * U * (1 + self.lse.abs())
         self.lse = torch.where(live, self.lse, 0.0)
         self.p = torch.where(live[:, None], torch.exp(self.s / tau - self.lse[:, None]), 0.0)
@@ -99,9 +110,14 @@ class Ref:
                                                               ((c * self.p).T @ self.x, (c * self.q).T @ self.x))]
         e_dx = e_g @ self.t.abs() + (6 * g.shape[1] + 64) * U * (g.abs() @ self.t.abs()) + 6 * g.shape[1] * TINY
         e_dt = e_g.T @ self.x.abs() + (6 * g.shape[0] + 64) * U * (g.abs().T @ self.x.abs()) + 6 * g.shape[0] * TINY
-        # a bf16 gradient of a float32 table or rows: products of two planes, 2^-15 of the terms at most
-        if g_type == F32 and xt == BF16:
-            e_dx = e_dx + 2.0 ** -14 * (g.abs() @ self.t.abs())
+        if self.halves:
+            e_dx = e_dx + STEP16 * (g.abs().sum(1, keepdim=True) * self.t.abs().max() + c.abs() * self.t.abs().sum(0))
+            cx = (c * self.x).abs()
+            one = (self.p - self.q).abs()
+            e_dt = e_dt + STEP16 * (one.sum(0)[:, None] * cx.max() + cx.sum(0)[None])
+            if xt == BF16:
+                e_dx = e_dx + 2.0 ** -10 * (g.abs() @ self.t.abs())
+        # a bf16 gradient beside float32 rows: products of two bf16 planes, 2^-15 of the terms at most
         if g_type == F32 and tt == BF16:
             e_dt = e_dt + 2.0 ** -14 * (g.abs().T @ self.x.abs())
         return dx, dt, e_dx + h(xt) * (dx.abs() + e_dx), e_dt + h(tt) * (dt.abs() + e_dt)
@@ -112,9 +128,10 @@ def gtype(xt, tt):
 
 
 def norm_tol(out, g, r):
-    """2-norm tolerance: the roundings of g and of the output where they are bf16, and the logits' 16 u."""
+    """2-norm tolerance: the roundings of g and of the output where they are bf16, of the leading fp16 values
+    where those stand alone, and the logits' 16 u."""
     roundings = (out == BF16) + (g == BF16)
-    return h(BF16) * roundings + 16 * U * (1 + float(r.s.abs().max()) / r.tau)
+    return h(BF16) * roundings + (2.0 ** -10 if r.halves and out == BF16 else 0.0) + 16 * U * (1 + float(r.s.abs().max()) / r.tau)
 
 
 def check_xent(mmf, x, t, targets, dloss, want=(True, True)):
