@@ -235,6 +235,14 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// two finite values (or NaN) at once
+__device__ __forceinline__ uint32_t peel_half2(float& a, float& b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  a -= f.x;
+  b -= f.y;
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 // 2^k that brings `most`, the largest finite magnitude, to [2^14, 2^15); within what a float32 holds.
 __device__ __forceinline__ float unit_up(float most) {
   int e = (int)(__float_as_uint(most) >> 23) - 127;  // floor(log2); -127 for zero and subnormals
@@ -344,11 +352,18 @@ __device__ __forceinline__ Tile tile_at(const Params& P, const Geo& G, int t) {
   return T;
 }
 
-// accumulators (segments of K) of a tile
+// Accumulators (segments of K) of a tile, and the k-blocks of one: FLUSH_KB of the leading planes'
+// product, the last in order. The products before it are 2^-8 or less of it, and so is what the
+// accumulator cuts off them: they all go into the first segment.
 template <bool FLUSH>
 __device__ __forceinline__ int tile_segments(const Tile& T) {
-  const int total = T.nprod * T.nkb;
-  return FLUSH && total > FLUSH_KB ? cdiv(total, FLUSH_KB) : 1;
+  return FLUSH && T.nkb > FLUSH_KB ? cdiv(T.nkb, FLUSH_KB) : 1;
+}
+template <bool FLUSH>
+__device__ __forceinline__ int segment_blocks(const Tile& T, int seg) {
+  if (!FLUSH) return T.nprod * T.nkb;
+  const int left = T.nkb - seg * FLUSH_KB;
+  return (seg == 0 ? (T.nprod - 1) * T.nkb : 0) + (left < FLUSH_KB ? left : FLUSH_KB);
 }
 
 template <int MODE, bool FLUSH>
@@ -466,12 +481,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         const Tile T = tile_at<MODE>(P, G, t);
         const bool a_mn = MODE == kProducts && T.kind == 0, b_mn = MODE == kProducts;
         const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-        const int total = T.nprod * T.nkb, segs = tile_segments<FLUSH>(T);
+        const int segs = tile_segments<FLUSH>(T);
         for (int seg = 0; ok && seg < segs; ++seg, ++n) {
           const uint32_t buf = n & 1u, acc = tmem + buf * BN;
           if (!mbar_wait_bounded(&accempty[buf], ((n >> 1) & 1u) ^ 1u, limit, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const int its = !FLUSH ? total : total - seg * FLUSH_KB < FLUSH_KB ? total - seg * FLUSH_KB : FLUSH_KB;
+          const int its = segment_blocks<FLUSH>(T, seg);
           for (int i = 0; i < its; ++i, ++it) {
             const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
             if (!mbar_wait_bounded(&full[s], ph, limit, abort_flag)) { ok = false; break; }
@@ -540,13 +555,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
         for (int e = 0; e < (FLUSH ? BN / 2 : 1); ++e) sum[e] = 0.0f;
       }
-      if (FLUSH && P.t_unit && (MODE != kProducts || T.kind == 0)) {
-        // dx's units go where its partials are added
-        const float u = MODE == kProducts ? *P.dt_unit * (1.0f / kGradUnit) : (row < live ? P.x_unit[row] : 0.0f);
-        const float ut = MODE == kProducts ? 1.0f : *P.t_unit;
-#pragma unroll
-        for (int e = 0; e < (FLUSH ? BN / 2 : 1); ++e) sum[e] = sum[e] * u * ut;
-      }
+      // the powers of two of fp16 operands: of the row and the table, or of dT's (dx's go where its
+      // partials are added)
+      float unit = 1.0f;
+      if (FLUSH && P.t_unit)
+        unit = MODE != kProducts ? (row < live ? P.x_unit[row] * *P.t_unit : 0.0f)
+               : T.kind == 0     ? *P.dt_unit * (1.0f / kGradUnit)
+                                 : 1.0f;
+      const float scale = P.scale * unit;
       // columns [c0, c0 + N) of D into v (with FLUSH they are in `sum` already)
       const auto cols32 = [&](int c0, float* v) {
         uint32_t w[32];
@@ -569,17 +585,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
           for (int e = 0; e < W; ++e)
             if (tgt == e) hit = sum[e];
-          P.st[row] = hit;
+          P.st[row] = hit * unit;
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int e = 0; e < W; ++e) m4[e & 3] = fmaxf(m4[e & 3], sum[e]);
         const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        const float off = top == -INFINITY ? 0.0f : -top * P.scale;
+        const float off = top == -INFINITY ? 0.0f : -top * scale;
 #pragma unroll
-        for (int e = 0; e < W; ++e) s4[e & 3] += ex2(fmaf(sum[e], P.scale, off));
+        for (int e = 0; e < W; ++e) s4[e & 3] += ex2(fmaf(sum[e], scale, off));
         if (row < live)
-          P.part[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+          P.part[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + row] = make_float2(top * unit, (s4[0] + s4[1]) + (s4[2] + s4[3]));
         if (P.top) {
           // the logits at the teacher's ids, while they are here: a group of 32 columns that holds one
           // of the warp's entries goes through the warp's staging rows, where it can be indexed
@@ -603,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
                            __float_as_uint(sum[FLUSH ? c0 + 4 * j + 3 : 0]));
             while (ent.x < begin + 32) {  // at most top_k entries; a row reads what its own thread wrote
               const uint32_t c = (uint32_t)(ent.x - begin);
-              P.s_top[base + ent.y] = ld_shared_f32(stg_row + (((c >> 2) << 4) ^ swz) + ((c & 3u) << 2));
+              P.s_top[base + ent.y] = unit * ld_shared_f32(stg_row + (((c >> 2) << 4) ^ swz) + ((c & 3u) << 2));
               ent = ++pos < P.top_k ? P.top[base + pos] : make_int2(0x7fffffff, 0);
             }
           }
@@ -615,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         const int tgt = P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
         const auto grads = [&](float* gv, int c0, int w) {
 #pragma unroll
-          for (int e = 0; e < w; ++e) gv[e] = ex2(fmaf(gv[e], P.scale, -lse2));
+          for (int e = 0; e < w; ++e) gv[e] = ex2(fmaf(gv[e], scale, -lse2));
           if ((uint32_t)(tgt - c0) < (uint32_t)w) {
 #pragma unroll
             for (int e = 0; e < w; ++e)
@@ -650,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
                 // keeps the compiler from splitting all values ahead of the stores, into spills
                 asm volatile("" : "+f"(a), "+f"(b));
                 if (!FLUSH) w[q] = pack_bf16_rn(a, b);
-                else if (halves) w[q] = pack_half(peel_half(a), peel_half(b));
+                else if (halves) w[q] = peel_half2(a, b);
                 else w[q] = pack_bf16_hi(peel(a), peel(b));
               }
               st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), w[0], w[1], w[2], w[3]);
@@ -675,6 +691,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           float own[FLUSH ? 1 : 32];
           float* v = FLUSH ? sum + (FLUSH ? c0 : 0) : own;
           if (!FLUSH) cols32(c0, v);
+          if (FLUSH) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= unit;
+          }
           const int h = f32 ? 0 : (c0 >> 5) & 1;  // bf16: two groups of 32 columns fill a 128-byte row
           if (h == 0) {
             if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
