@@ -366,8 +366,10 @@ __device__ __forceinline__ int segment_blocks(const Tile& T, int seg) {
   return (seg == 0 ? (T.nprod - 1) * T.nkb : 0) + (left < FLUSH_KB ? left : FLUSH_KB);
 }
 
-template <int MODE, bool FLUSH>
+// GP (kGrad, kProducts): planes of g, 1 (bf16), 3 (bf16, exact) or 2 (fp16).
+template <int MODE, int GP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_constant__ Params P) {
+  constexpr bool FLUSH = MODE == kStats || GP > 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + STAGES * STAGE_BYTES;
@@ -626,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         }
       } else if (MODE == kGrad) {
         // pad rows have c = lse = 0: zeros, which the products over the live rows rely on
-        const bool halves = FLUSH && P.t_unit;
+        constexpr bool halves = GP == 2;
         const float c = !halves ? P.c[row] : row < live ? kGradUnit : 0.0f, lse2 = P.lse[row] * kLog2e;
         const int tgt = P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
         const auto grads = [&](float* gv, int c0, int w) {
@@ -652,8 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
             grads(gv, c0, FLUSH ? 0 : 64);
           }
 #pragma unroll
-          for (int p = 0; p < (FLUSH ? PLANES : 1); ++p) {
-            if (FLUSH && p == 2 && halves) break;
+          for (int p = 0; p < GP; ++p) {
             if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
             __syncwarp();
 #pragma unroll

@@ -148,11 +148,12 @@ cudaError_t head_loss_attrs() {
   auto set = [&](const void* f, int smem) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
-  set((const void*)hl::head_loss_kernel<hl::kStats, true>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kGrad, false>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kGrad, true>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kProducts, false>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kProducts, true>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kStats, 1>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, 1>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, 2>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, 3>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kProducts, 1>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kProducts, 2>, hl::SMEM_BYTES);
   return e;
 }
 
@@ -1260,9 +1261,9 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   return MMF_OK;
 }
 
-template <int MODE, bool FLUSH>
+template <int MODE, int GP>
 void loss_launch(const hl::Params& P, const DevInfo& di, cudaStream_t st) {
-  launch_after(hl::head_loss_kernel<MODE, FLUSH>, dim3((unsigned)di.sms & ~1u), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
+  launch_after(hl::head_loss_kernel<MODE, GP>, dim3((unsigned)di.sms & ~1u), dim3(hl::THREADS), hl::SMEM_BYTES, st, P);
 }
 
 mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top, void* ws, size_t ws_bytes,
@@ -1291,7 +1292,7 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
   P.rowmap = L.rowmap;
   P.s_top = s_top;
   P.top_k = a.teacher.k;
-  loss_launch<hl::kStats, true>(P, *di, st);
+  loss_launch<hl::kStats, 1>(P, *di, st);
   launch_after(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
            L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
            1.0f / a.tau, loss, lse);
@@ -1363,8 +1364,9 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
     MMF_TRY(encode_3d(&P.g_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.g, P.vn, L.m_pad, L.pg, grow, L.m_pad * grow, 64, 32));
     P.dx_plane0 = i * L.dx_split;
     P.dt_row0 = P.v0;
-    if (L.pg == 1) loss_launch<hl::kGrad, false>(P, *di, st);
-    else loss_launch<hl::kGrad, true>(P, *di, st);
+    if (L.pg == 1) loss_launch<hl::kGrad, 1>(P, *di, st);
+    else if (L.pg == 2) loss_launch<hl::kGrad, 2>(P, *di, st);
+    else loss_launch<hl::kGrad, 3>(P, *di, st);
     if (!a.targets) {
       launch_after(hl::teacher_grad_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
                (const int2*)L.top, (const float*)L.q, a.teacher.k, a.teacher.inv_tau, (const int32_t*)L.live,
@@ -1372,8 +1374,8 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
       ++launches;
     }
     if (halves) P.x = weighed;
-    if (L.pg == 1) loss_launch<hl::kProducts, false>(P, *di, st);
-    else loss_launch<hl::kProducts, true>(P, *di, st);
+    if (L.pg == 1) loss_launch<hl::kProducts, 1>(P, *di, st);
+    else loss_launch<hl::kProducts, 2>(P, *di, st);
     P.x = rows;
     launches += 2;
   }
