@@ -610,9 +610,10 @@ def _scratch(op: int, m: int, d: int, inner: int, bits: int, device: torch.devic
 
 def _together(first: torch.Tensor, **others: torch.Tensor | None) -> None:
     """Every tensor of a call has to be on one device."""
+    device = first.device
     for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name}: on {t.device}, expected {first.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
 def rmsnorm_fwd(x: torch.Tensor, norm_w: torch.Tensor | None, eps: float = 1e-8,
@@ -625,7 +626,7 @@ def rmsnorm_fwd(x: torch.Tensor, norm_w: torch.Tensor | None, eps: float = 1e-8,
     d = x.shape[-1]
     _f32(norm_w, (d,), "norm_w")
     _together(x, norm_w=norm_w)
-    y = torch.empty(x.shape, dtype=y_dtype or x.dtype, device=x.device)
+    y = torch.empty_like(x, dtype=y_dtype)
     with _on(x.device):
         _check(lib().mmf_rmsnorm_fwd(x.data_ptr(), _dt(x.dtype), x.numel() // d, d, _ptr(norm_w), eps, y.data_ptr(),
                                      _dt(y.dtype), _stream(x.device)), "mmf_rmsnorm_fwd")
@@ -682,8 +683,8 @@ def lm_head_xent_fwd(x: torch.Tensor, table: torch.Tensor, targets: torch.Tensor
     if tuple(_i32(targets, "targets").shape) != (m,):
         raise ValueError(f"targets: expected [{m}], got {tuple(targets.shape)}")
     _together(x, targets=targets)
-    loss = torch.empty(m, dtype=torch.float32, device=x.device)
-    lse = torch.empty(m, dtype=torch.float32, device=x.device)
+    loss = x.new_empty(m, dtype=torch.float32)
+    lse = x.new_empty(m, dtype=torch.float32)
     with _on(x.device):
         ws = _scratch(MMF_OP_HEAD_LOSS, m, d, vocab, bits, x.device)
         _check(lib().mmf_lm_head_xent_fwd(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(), _dt(table.dtype), vocab,
@@ -720,9 +721,9 @@ def lm_head_distill_fwd(x: torch.Tensor, table: torch.Tensor, t_ids: torch.Tenso
     Entries with an id outside [0, vocab) or a logit of -inf do not count."""
     m, d, vocab, bits = _head_loss_args(x, table)
     k = _teacher_args(x, t_ids, t_logits)
-    loss = torch.empty(m, dtype=torch.float32, device=x.device)
-    lse = torch.empty(m, dtype=torch.float32, device=x.device)
-    s_top = torch.empty(m, k, dtype=torch.float32, device=x.device)
+    loss = x.new_empty(m, dtype=torch.float32)
+    lse = x.new_empty(m, dtype=torch.float32)
+    s_top = x.new_empty((m, k), dtype=torch.float32)
     with _on(x.device):
         ws = _scratch(MMF_OP_HEAD_LOSS, m, d, vocab, bits + 4 * k, x.device)
         _check(lib().mmf_lm_head_distill_fwd(x.data_ptr(), _dt(x.dtype), m, d, table.data_ptr(), _dt(table.dtype),

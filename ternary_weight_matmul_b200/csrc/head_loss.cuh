@@ -1199,92 +1199,73 @@ __device__ __forceinline__ void teacher_softmax(const Teacher& t, int64_t r, int
   total = warp_sum(total);
 }
 
-constexpr int kTeacherRows = 32;      // rows per CTA, one warp each
+constexpr int kTeacherRows = 16;      // rows per CTA, one warp each
 constexpr int kTeacherTiles = 128;    // tile halves per turn
 // Per row: its live flag (it has a valid entry), and its entries in order of their ids (equal ids in
 // order of the entries), entries that are not valid last with id 2^31 - 1. The place of an entry is the
-// number of entries before it, counted over the row in shared memory.
-//   starts (forward): start[h][r] = entries with an id below 128 h, so that the tile half at columns
-//     128 h finds its own without a search, and zeros in s_top at entries that are not valid;
+// number of entries before it, counted over the row in shared memory, four at a time.
+//   start (forward): start[h][r] = valid entries with an id below 128 h, so that the tile half at
+//     columns 128 h finds its own without a search, and zeros in s_top at entries that are not valid;
 //   q (backward): the teacher's weight of every entry, in the same order.
-__global__ void __launch_bounds__(kTeacherRows * 32) teacher_rows_kernel(const Teacher t, int64_t m, int64_t m_pad,
-                                                                         int halves, uint8_t* __restrict__ flags,
-                                                                         int2* __restrict__ top,
-                                                                         uint16_t* __restrict__ start,
-                                                                         float* __restrict__ s_top,
-                                                                         float* __restrict__ q) {
-  dependent();
+__global__ void __launch_bounds__(kTeacherRows * 32, 3) teacher_rows_kernel(const Teacher t, int64_t m, int64_t m_pad,
+                                                                            int halves, uint8_t* __restrict__ flags,
+                                                                            int2* __restrict__ top,
+                                                                            uint16_t* __restrict__ start,
+                                                                            float* __restrict__ s_top,
+                                                                            float* __restrict__ q) {
   __shared__ __align__(16) int32_t ids[kTeacherRows][MAX_TOP];
+  __shared__ int32_t sorted[kTeacherRows][MAX_TOP];
   __shared__ uint16_t turn[kTeacherTiles][kTeacherRows + 1];
+  dependent();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t r0 = (int64_t)blockIdx.x * kTeacherRows, r = r0 + warp;
-  constexpr int PER = MAX_TOP / 32;
   constexpr int32_t kNone = 0x7fffffff;
-  int32_t id[PER];
-  int place[PER];
-  bool any = false;
-#pragma unroll
-  for (int u = 0; u < PER; ++u) {
-    const int j = u * 32 + lane;
-    id[u] = kNone;
-    if (r < m && j < t.k) {
-      float l;
-      const bool valid = teacher_valid(t, r * t.k + j, l);
-      if (valid) id[u] = t.ids[r * t.k + j];
-      any |= valid;
-      if (s_top && !valid) s_top[r * t.k + j] = 0.0f;
-    }
-    if (u * 32 < t.k) ids[warp][j] = id[u];  // past the row's entries: no id, counted by nobody
-  }
-  any = __any_sync(0xffffffffu, any);
-  if (r < m && lane == 0) flags[r] = any ? 1 : 0;
-  __syncwarp();
+  int count = 0;  // valid entries
   if (r < m) {
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int j = u * 32 + lane;
-      place[u] = 0;
-      if (u * 32 < t.k)
-        for (int i = 0; i < t.k; i += 4) {
-          const int4 o = *reinterpret_cast<const int4*>(&ids[warp][i]);
-          const int32_t o4[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) place[u] += o4[e] < id[u] || (o4[e] == id[u] && i + e < j) ? 1 : 0;
-        }
+    for (int j = lane; j < ((t.k + 31) & ~31); j += 32) {
+      float l;
+      int32_t id = kNone;  // past the row's entries too: counted by nobody
+      if (j < t.k) {
+        const int32_t given = t.ids[r * t.k + j];
+        if (teacher_valid(t, r * t.k + j, l)) id = given;
+        else if (s_top) s_top[r * t.k + j] = 0.0f;
+      }
+      ids[warp][j] = id;
+      count += __popc(__ballot_sync(0xffffffffu, id != kNone));
     }
+    if (lane == 0) flags[r] = count > 0 ? 1 : 0;
     float best = 0.0f, total = 1.0f;
     if (q) teacher_softmax(t, r, lane, best, total);
     __syncwarp();
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const int j = u * 32 + lane;
-      if (j < t.k) {
-        ids[warp][place[u]] = id[u];
-        top[r * t.k + place[u]] = make_int2(id[u], j);
-        if (q) {
-          float l;
-          const bool valid = teacher_valid(t, r * t.k + j, l);
-          q[r * t.k + place[u]] = valid ? expf((l - best) * t.inv_tau) / total : 0.0f;
-        }
+    for (int j = lane; j < t.k; j += 32) {
+      const int32_t id = ids[warp][j];
+      int place = 0;
+      for (int i = 0; i < t.k; i += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(&ids[warp][i]);
+        place += (o.x < id || (o.x == id && i < j)) + (o.y < id || (o.y == id && i + 1 < j)) +
+                 (o.z < id || (o.z == id && i + 2 < j)) + (o.w < id || (o.w == id && i + 3 < j));
       }
+      sorted[warp][place] = id;
+      top[r * t.k + place] = make_int2(id, j);
+      if (q)
+        q[r * t.k + place] = id != kNone ? expf((load_as_float(t.logits, r * t.k + j, t.dt) - best) * t.inv_tau) / total : 0.0f;
     }
   }
   if (!start) return;  // uniform
   __syncwarp();
+  // the first entry of half h is the first one whose own half is h or later: entry p is it for the
+  // halves past entry p - 1's up to its own, and the end of the row for those past the last entry's
   for (int h0 = 0; h0 < halves; h0 += kTeacherTiles) {
-    for (int h = lane; h < kTeacherTiles; h += 32) {
-      int lo = 0, hi = r < m ? t.k : 0;
-      const int64_t bound = (int64_t)(h0 + h) * (BN / 2);
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (ids[warp][mid] < bound) lo = mid + 1;
-        else hi = mid;
-      }
-      turn[h][warp] = (uint16_t)lo;
+    for (int p = lane; p <= count; p += 32) {
+      const int from = p == 0 ? h0 : max(sorted[warp][p - 1] / (BN / 2) + 1, h0);
+      const int to = min(p == count ? h0 + kTeacherTiles - 1 : sorted[warp][p] / (BN / 2), h0 + kTeacherTiles - 1);
+      for (int h = from; h <= to; ++h) turn[h - h0][warp] = (uint16_t)p;
     }
     __syncthreads();
-    for (int h = warp; h < kTeacherTiles && h0 + h < halves; h += kTeacherRows)
-      if (r0 + lane < m_pad) start[(int64_t)(h0 + h) * m_pad + r0 + lane] = turn[h][lane];
+    for (int e = threadIdx.x; e < kTeacherTiles * kTeacherRows; e += kTeacherRows * 32) {
+      const int h = e / kTeacherRows, i = e % kTeacherRows;
+      if (h0 + h < halves && r0 + i < m_pad) start[(int64_t)(h0 + h) * m_pad + r0 + i] = turn[h][i];
+    }
     __syncthreads();
   }
 }
