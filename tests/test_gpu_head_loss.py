@@ -167,7 +167,8 @@ IDS = ["bf16", "f32", "f32-bf16", "bf16-f32"]
 
 @pytest.mark.parametrize("xt,tt", TYPES, ids=IDS)
 @pytest.mark.parametrize("m,d,v", [(1, 8, 1), (1, 1024, 32000), (2, 64, 2), (31, 72, 257), (128, 128, 256),
-                                   (129, 136, 1000), (300, 704, 5003), (513, 256, 255)])
+                                   (129, 136, 1000), (300, 704, 5003), (513, 256, 255), (200, 72, 257),
+                                   (256, 704, 2000), (769, 136, 1000), (1500, 1032, 513)])
 def test_xent_shapes_and_types(mmf, m, d, v, xt, tt):
     x, t, g = operands(m * 31 + v, m, d, v, xt, tt)
     targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
@@ -186,8 +187,9 @@ def test_xent_several_vocabulary_pieces(mmf, xt, tt, m, v):
 
 @pytest.mark.parametrize("xt,tt", TYPES[:2], ids=IDS[:2])
 @pytest.mark.parametrize("pattern", ["none", "one", "last", "alternate", "out of range"])
-def test_xent_rows_left_out(mmf, xt, tt, pattern):
-    m, d, v = 515, 128, 700
+@pytest.mark.parametrize("m", [515, 1030, 5001])
+def test_xent_rows_left_out(mmf, m, xt, tt, pattern):
+    d, v = 128, 700
     x, t, g = operands(11, m, d, v, xt, tt)
     targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
     drop = torch.ones(m, dtype=torch.bool, device=DEV)
@@ -231,8 +233,9 @@ def test_xent_one_sided_gradients_and_no_rows(mmf):
     assert dx.shape == (0, 64) and not dt.any() and dt.shape == t.shape
 
 
-def test_xent_large_logits_and_nan_stay_in_their_rows(mmf):
-    m, d, v = 130, 64, 400
+@pytest.mark.parametrize("m", [130, 800])
+def test_xent_large_logits_and_nan_stay_in_their_rows(mmf, m):
+    d, v = 64, 400
     x, t, g = operands(13, m, d, v, BF16, BF16, spread=200.0)  # logits of several hundred
     targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
     check_xent(mmf, x, t, targets, torch.randn(m, generator=g, device=DEV))
@@ -245,6 +248,17 @@ def test_xent_large_logits_and_nan_stay_in_their_rows(mmf):
     dx, _ = mmf.lm_head_xent_backward(x, t, targets, lse, torch.ones(m, device=DEV), want_dtable=False)
     assert torch.isfinite(dx[~bad]).all() and not torch.isfinite(dx[bad]).all(1).any()
     assert mmf.sync_status(DEV) == mmf.MMF_OK
+
+
+@pytest.mark.parametrize("m", [90, 900])
+@pytest.mark.parametrize("up", [1e18, 1e-18])
+def test_xent_float32_magnitudes(mmf, m, up):
+    """Operands far from one with logits of order one: the fp16 pairs' powers of two at work."""
+    x, t, g = operands(14, m, 128, 600, F32, F32)
+    x[3] *= 1e-3
+    targets = torch.randint(0, 600, (m,), generator=g, device=DEV).to(torch.int32)
+    check_xent(mmf, x * up, t / up, targets, torch.randn(m, generator=g, device=DEV))
+    check_xent(mmf, x, t, targets, torch.randn(m, generator=g, device=DEV) * up)
 
 
 def teacher_ref(ids, logits, v, tau):
@@ -295,7 +309,8 @@ def teacher(seed, m, k, v, dtype):
 
 @pytest.mark.parametrize("xt,tt", TYPES, ids=IDS)
 @pytest.mark.parametrize("m,d,v,k,tau", [(1, 8, 1, 1, 1.0), (1, 1024, 32000, 64, 2.0), (33, 72, 257, 5, 0.5),
-                                         (129, 128, 1000, 33, 1.0), (300, 256, 5003, 256, 3.0)])
+                                         (129, 128, 1000, 33, 1.0), (300, 256, 5003, 256, 3.0),
+                                         (200, 72, 257, 5, 0.5), (900, 264, 1100, 40, 2.0)])
 def test_distill_shapes_and_types(mmf, m, d, v, k, tau, xt, tt):
     x, t, _ = operands(m * 17 + v, m, d, v, xt, tt)
     ids, logits, dloss = teacher(m + k, m, k, v, tt)
@@ -310,8 +325,9 @@ def test_distill_several_vocabulary_pieces(mmf):
 
 
 @pytest.mark.parametrize("lt", [F32, BF16])
-def test_distill_masked_entries(mmf, lt):
-    m, d, v, k = 260, 64, 500, 40
+@pytest.mark.parametrize("m", [260, 1000])
+def test_distill_masked_entries(mmf, m, lt):
+    d, v, k = 64, 500, 40
     x, t, _ = operands(23, m, d, v, BF16, BF16)
     ids, logits, dloss = teacher(24, m, k, v, lt)
     low = torch.finfo(lt).min
@@ -461,8 +477,9 @@ def test_run_through_the_model(mmf):
     assert torch.allclose(torch.logsumexp(logits.double(), 1)[targets >= 0], lse[targets >= 0].double(), rtol=1e-4)
 
 
-def test_repeats_streams_and_graphs(mmf):
-    m, d, v, k = 700, 256, 3001, 24
+@pytest.mark.parametrize("m", [70, 700])
+def test_repeats_streams_and_graphs(mmf, m):
+    d, v, k = 256, 3001, 24
     x, t, g = operands(51, m, d, v, BF16, BF16)
     targets = torch.randint(-300, v, (m,), generator=g, device=DEV).to(torch.int32)
     ids, logits, dloss = teacher(52, m, k, v, BF16)
@@ -511,10 +528,11 @@ def test_repeats_streams_and_graphs(mmf):
     assert mmf.sync_status(DEV) == mmf.MMF_OK
 
 
-def test_waits_that_run_out_are_reported(mmf):
+@pytest.mark.parametrize("m", [300, 2000])
+def test_waits_that_run_out_are_reported(mmf, m):
     """With the cap at one microsecond the kernels' waits may run out: the call then ends by itself
     and the status says so; with the default cap the same call is right again."""
-    m, d, v = 2000, 512, 9000
+    d, v = 512, 9000
     x, t, g = operands(61, m, d, v, BF16, BF16)
     targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
     dloss = torch.randn(m, generator=g, device=DEV)
