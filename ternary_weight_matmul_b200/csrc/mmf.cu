@@ -149,9 +149,11 @@ cudaError_t head_loss_attrs() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
   set((const void*)hl::head_loss_kernel<hl::kStats, 1>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kGrad, 1>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kGrad, 2>, hl::SMEM_BYTES);
-  set((const void*)hl::head_loss_kernel<hl::kGrad, 3>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kStats, 2>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, hl::kOne>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, hl::kHalf2>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, hl::kExact3>, hl::SMEM_BYTES);
+  set((const void*)hl::head_loss_kernel<hl::kGrad, hl::kFine2>, hl::SMEM_BYTES);
   set((const void*)hl::head_loss_kernel<hl::kProducts, 1>, hl::SMEM_BYTES);
   set((const void*)hl::head_loss_kernel<hl::kProducts, 2>, hl::SMEM_BYTES);
   return e;
@@ -1034,6 +1036,10 @@ constexpr int kLossPairs = 74;         // CTA pairs at work at once
 constexpr int kLossSplitBlocks = 8;    // a K split has at least this many 64-wide k-blocks
 constexpr int kLossTileBlocks = 4;     // a tile's epilogue, in k-blocks' time
 constexpr int kLossMaxSplit = 64;
+// Up to so many bf16 rows g is held in two bf16 values: with few rows the roundings that lead each row of
+// g are too few to average (1.7e-3 of dx, each up to 3.9e-3), and the products wait for HBM more than
+// for the MMA (forward + backward of 40 rows: @FINE@).
+constexpr int kLossFineRows = 128;
 constexpr int32_t kHeadLossMaxD = 32768;
 
 // K splits of a product with `tiles` tiles of `kb` k-blocks, where the tiles alone leave pairs idle:
@@ -1057,7 +1063,8 @@ inline int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct LossPlan {
   int64_t m_pad;
-  int32_t px, pt, pg;       // bf16 planes of x, the table and g
+  int32_t px, pt, pg;       // planes of x, the table and g
+  int gp;                   // hl::GradPlanes
   int32_t parts;            // statistics parts per row
   int64_t piece, ldg;       // vocabulary columns per piece, row pitch of g
   int32_t pieces, dx_split, dt_split;
@@ -1099,7 +1106,8 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   L.m_pad = (m + 255) / 256 * 256;
   L.px = xf32 ? (tf32 ? 2 : hl::PLANES) : 1;
   L.pt = tf32 ? 2 : 1;
-  L.pg = tf32 ? 2 : xf32 ? hl::PLANES : 1;
+  L.gp = tf32 ? hl::kHalf2 : xf32 ? hl::kExact3 : m <= kLossFineRows ? hl::kFine2 : hl::kOne;
+  L.pg = hl::grad_planes(L.gp);
   const size_t M = (size_t)L.m_pad;
   L.live = reinterpret_cast<int32_t*>(take(sizeof(int32_t)));
   L.rowmap = reinterpret_cast<int32_t*>(take(M * 4));
@@ -1292,7 +1300,8 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
   P.rowmap = L.rowmap;
   P.s_top = s_top;
   P.top_k = a.teacher.k;
-  loss_launch<hl::kStats, 1>(P, *di, st);
+  if (L.px == 1 && L.pt == 1) loss_launch<hl::kStats, 1>(P, *di, st);
+  else loss_launch<hl::kStats, 2>(P, *di, st);
   launch_after(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
            L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
            1.0f / a.tau, loss, lse);
@@ -1334,8 +1343,8 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
   // a float32 result takes every pair; a bf16 one of three bf16 planes the pairs above 2^-15, of fp16
   // planes (2^-12 each) the first alone
   const bool halves = a.tdt == MMF_F32;
-  P.dxp = loss_prods(L.pg, L.pt, halves ? (a.xdt == MMF_F32 ? 1 : 0) : L.pg == 1 ? 0 : 2);
-  P.dtp = loss_prods(L.pg, halves ? 2 : L.px, halves || L.pg > 1 ? 1 : 0);
+  P.dxp = loss_prods(L.pg, L.pt, halves ? (a.xdt == MMF_F32 ? 1 : 0) : L.pg - 1);
+  P.dtp = loss_prods(L.pg, halves ? 2 : L.px, L.pg > 1 ? 1 : 0);
   CUtensorMap weighed;
   if (halves)
     MMF_TRY(encode_3d(&weighed, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.xw, a.d, L.m_pad, 2, (uint64_t)a.d * 2,
@@ -1364,17 +1373,18 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
     MMF_TRY(encode_3d(&P.g_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.g, P.vn, L.m_pad, L.pg, grow, L.m_pad * grow, 64, 32));
     P.dx_plane0 = i * L.dx_split;
     P.dt_row0 = P.v0;
-    if (L.pg == 1) loss_launch<hl::kGrad, 1>(P, *di, st);
-    else if (L.pg == 2) loss_launch<hl::kGrad, 2>(P, *di, st);
-    else loss_launch<hl::kGrad, 3>(P, *di, st);
+    if (L.gp == hl::kOne) loss_launch<hl::kGrad, hl::kOne>(P, *di, st);
+    else if (L.gp == hl::kFine2) loss_launch<hl::kGrad, hl::kFine2>(P, *di, st);
+    else if (L.gp == hl::kHalf2) loss_launch<hl::kGrad, hl::kHalf2>(P, *di, st);
+    else loss_launch<hl::kGrad, hl::kExact3>(P, *di, st);
     if (!a.targets) {
       launch_after(hl::teacher_grad_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
                (const int2*)L.top, (const float*)L.q, a.teacher.k, a.teacher.inv_tau, (const int32_t*)L.live,
-               (const int32_t*)L.rowmap, s_top, (const float*)L.c, (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.pg);
+               (const int32_t*)L.rowmap, s_top, (const float*)L.c, (const float*)L.lse, P.v0, P.vn, L.g, L.m_pad, L.ldg, L.gp);
       ++launches;
     }
     if (halves) P.x = weighed;
-    if (L.pg == 1) loss_launch<hl::kProducts, 1>(P, *di, st);
+    if (L.gp == hl::kOne || L.gp == hl::kFine2) loss_launch<hl::kProducts, 1>(P, *di, st);
     else loss_launch<hl::kProducts, 2>(P, *di, st);
     P.x = rows;
     launches += 2;

@@ -124,6 +124,8 @@ class Ref:
 
 
 def gtype(xt, tt):
+    """What g is held to: one bf16 value with bf16 operands (finer in calls of few rows, which the bound
+    for one value covers)."""
     return BF16 if xt == BF16 and tt == BF16 else F32
 
 
