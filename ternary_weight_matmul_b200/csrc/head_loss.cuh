@@ -113,6 +113,10 @@ struct Params {
   const float* t_unit;          // of the table
   const float* dt_unit;         // of c x
   int32_t dt_row0;              // first row of dt_out this launch writes
+  // kProducts with few rows: dx^T = T^T g^T, so that M is 256 columns of d and N the rows, in 64s; with
+  // 256 rows as M, 40 of them cost what 256 do
+  int32_t few_n;                // N, or 0
+  float* dx_part;               // dx_out's array
   uint32_t wait_limit_us;
 };
 
@@ -282,8 +286,9 @@ struct Tile {
   int row, col;     // first row / column of D
   int kb0, nkb;     // k-blocks (per plane pair)
   int nprod;
-  int kind;         // kProducts: 0 = dT, 1 = dx; else 0
+  int kind;         // kProducts: 0 = dT, 1 = dx, 2 = dx of few rows; else 0
   int split;
+  int n;            // columns of D (MMA N)
 };
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return a / b + (a % b != 0); }
@@ -291,7 +296,7 @@ __host__ __device__ __forceinline__ int cdiv(int a, int b) { return a / b + (a %
 // What all tiles of a launch share, worked out once per thread.
 struct Geo {
   int tiles;
-  int nt;                  // column tiles
+  int nt, nt_dx;           // column tiles
   int mt;                  // row tiles (kStats, kGrad)
   int kb_d;                // k-blocks of d
   int per_dt, per_dx, end_dt;  // kProducts: tiles per split, tiles of dT
@@ -309,7 +314,8 @@ __device__ __forceinline__ Geo geometry(const Params& P, int live) {
   } else {
     G.nt = cdiv(P.d, BN);
     G.per_dt = cdiv(P.vn, BM) * G.nt;
-    G.per_dx = cdiv(live, BM) * G.nt;
+    G.nt_dx = P.few_n > 0 ? 1 : G.nt;
+    G.per_dx = P.few_n > 0 ? (live > 0 ? cdiv(P.d, BM) : 0) : cdiv(live, BM) * G.nt;
     G.end_dt = P.dt_split * G.per_dt;
     G.tiles = G.end_dt + P.dx_split * G.per_dx;
     G.kb_dt = cdiv(live, BK);
@@ -325,6 +331,7 @@ __device__ __forceinline__ Tile tile_at(const Params& P, const Geo& G, int t) {
   Tile T;
   T.kind = 0;
   T.split = 0;
+  T.n = BN;
   if (MODE != kProducts) {
     // groups of eight row tiles, columns slow inside a group: the pairs of one wave share a few row
     // tiles and a few table tiles, which the L2 then serves
@@ -339,7 +346,7 @@ __device__ __forceinline__ Tile tile_at(const Params& P, const Geo& G, int t) {
     T.nprod = P.fwd.n;
     return T;
   }
-  int kb, len, rem;
+  int kb, len, rem, nt = G.nt;
   if (t < G.end_dt) {
     T.split = P.dt_split > 1 ? t / G.per_dt : 0;
     rem = t - T.split * G.per_dt;
@@ -354,10 +361,15 @@ __device__ __forceinline__ Tile tile_at(const Params& P, const Geo& G, int t) {
     kb = G.kb_dx;
     len = G.len_dx;
     T.nprod = P.dxp.n;
+    nt = G.nt_dx;
+    if (P.few_n > 0) {
+      T.kind = 2;
+      T.n = P.few_n;
+    }
   }
-  const int m = rem / G.nt;
+  const int m = rem / nt;
   T.row = m * BM;
-  T.col = (rem - m * G.nt) * BN;
+  T.col = (rem - m * nt) * BN;
   T.kb0 = T.split * len;
   T.nkb = kb - T.kb0 < len ? kb - T.kb0 : len;
   if (T.nkb < 0) T.nkb = 0;
@@ -456,9 +468,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
             const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BOXES * BOX_BYTES;
             const int k = (T.kb0 + kb) * BK;
             const uint32_t bar = in_first_cta(&full[s]);
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * STAGE_BYTES);
-            const int arow = T.row + CM * (int)rank, bcol = T.col + BN / 2 * (int)rank;
-            if (MODE != kProducts) {
+            const int b_boxes = MODE == kProducts && T.n <= 128 ? 1 : B_BOXES;
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (A_BOXES + b_boxes) * BOX_BYTES);
+            const int arow = T.row + CM * (int)rank, bcol = T.col + T.n / 2 * (int)rank;
+            if (MODE == kProducts && T.kind == 2) {  // A MN-major, B K-major, k = vocabulary
+#pragma unroll
+              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.t, arow + 64 * i, P.v0 + k, pb, bar);
+              for (int i = 0; i < b_boxes; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.g, k, bcol + 64 * i, pa, bar);
+            } else if (MODE != kProducts) {
 #pragma unroll
               for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, arow + 64 * i, pa, bar);
 #pragma unroll
@@ -498,14 +515,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
       // kind::f16: D float32 (bits 4-5 = 1), A and B bf16 or fp16 (bits 7-9, 10-12), MN-major A / B at
       // bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28
       const uint32_t fmt = P.t_unit ? 0u : 1u;  // fp16 : bf16
-      const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(BN >> 3) << 17) |
-                              ((uint32_t)(BM >> 4) << 24);
+      const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(BM >> 4) << 24);
       uint32_t it = 0, n = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += stride) {
         const Tile T = tile_at<MODE>(P, G, t);
-        const bool a_mn = MODE == kProducts && T.kind == 0, b_mn = MODE == kProducts;
-        const uint32_t idesc = idesc0 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+        const bool a_mn = MODE == kProducts && T.kind != 1, b_mn = MODE == kProducts && T.kind != 2;
+        const uint32_t idesc = idesc0 | ((uint32_t)(T.n >> 3) << 17) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const int segs = tile_segments<FLUSH, KB>(T);
         for (int seg = 0; ok && seg < segs; ++seg, ++n) {
           const uint32_t buf = n & 1u, acc = tmem + buf * BN;
@@ -548,7 +564,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
     for (int t = first; ok && t < tiles; t += stride) {
       const Tile T = tile_at<MODE>(P, G, t);
       const int row0 = T.row + CM * (int)rank + quarter * 32, row = row0 + lane;
-      const int col0 = T.col + half * (BN / 2);
+      const int nh = MODE == kProducts ? T.n / 2 : BN / 2;  // columns of this half
+      const int col0 = T.col + half * nh;
       const bool zero = T.nprod * T.nkb == 0;  // no k-blocks: the accumulator was never written
       uint32_t acc = 0;
       float sum[FLUSH ? BN / 2 : 1];
@@ -559,10 +576,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         const bool have = mbar_wait_bounded(&accfull[buf], (n >> 1) & 1u, limit, abort_flag);
         if (!__all_sync(0xffffffffu, have)) { ok = false; break; }
         tc_fence_after();
-        acc = tmem + buf * BN + half * (BN / 2) + ((uint32_t)(quarter * 32) << 16);
+        acc = tmem + buf * BN + half * nh + ((uint32_t)(quarter * 32) << 16);
         if (FLUSH) {
 #pragma unroll
           for (int c0 = 0; c0 < BN / 2; c0 += 16) {
+            if (MODE == kProducts && c0 >= nh) break;
             uint32_t w[16];
             tmem_ld_32x32b_x16(acc + c0, w);
             tmem_wait_ld();
@@ -707,6 +725,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
             next_buffer();
           }
         }
+        }
+      } else if (T.kind == 2) {
+        // lane = column of d, column = row: a row's 32 values leave as 128 bytes
+        const int dcol = T.row + CM * (int)rank + quarter * 32 + lane;
+        float* o = P.dx_part + ((int64_t)(P.dx_plane0 + T.split) * P.m_pad + col0) * P.d + dcol;
+#pragma unroll
+        for (int c0 = 0; c0 < BN / 2; c0 += 32) {
+          if (c0 >= nh || col0 + c0 >= live) break;
+          float own[FLUSH ? 1 : 32];
+          float* v = FLUSH ? sum + (FLUSH ? c0 : 0) : own;
+          if (!FLUSH) cols32(c0, v);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (dcol < P.d && col0 + c0 + e < live) o[(int64_t)(c0 + e) * P.d] = v[e];
         }
       } else {
         const int rows = T.kind ? (int)P.m_pad : P.vn;

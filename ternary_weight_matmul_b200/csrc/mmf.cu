@@ -1036,6 +1036,7 @@ constexpr int kLossPairs = 74;         // CTA pairs at work at once
 constexpr int kLossSplitBlocks = 8;    // a K split has at least this many 64-wide k-blocks
 constexpr int kLossTileBlocks = 4;     // a tile's epilogue, in k-blocks' time
 constexpr int kLossMaxSplit = 64;
+constexpr int kLossFewRows = 192;      // dx with the rows as N: up to three quarters of a tile's 256
 // Up to so many bf16 rows g is held in two bf16 values: with few rows the roundings that lead each row of
 // g are too few to average (1.7e-3 of dx, each up to 3.9e-3), and the products wait for HBM more than
 // for the MMA (forward + backward of 40 rows: @FINE@).
@@ -1065,6 +1066,7 @@ struct LossPlan {
   int64_t m_pad;
   int32_t px, pt, pg;       // planes of x, the table and g
   int gp;                   // hl::GradPlanes
+  int32_t few_n;            // rows as N of dx's tiles, or 0
   int32_t parts;            // statistics parts per row
   int64_t piece, ldg;       // vocabulary columns per piece, row pitch of g
   int32_t pieces, dx_split, dt_split;
@@ -1146,7 +1148,8 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   L.pieces = (int32_t)((vocab + L.piece - 1) / L.piece);
   L.ldg = L.piece;
   const int64_t nt = cdiv64(d, hl::BN);
-  L.dx_split = loss_splits(L.m_pad / hl::BM * nt, L.piece / hl::BK);
+  if (m <= kLossFewRows) L.few_n = (int32_t)(cdiv64(std::max<int64_t>(m, 1), 64) * 64);
+  L.dx_split = loss_splits(L.few_n > 0 ? cdiv64(d, hl::BM) : L.m_pad / hl::BM * nt, L.piece / hl::BK);
   L.dt_split = loss_splits(cdiv64(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
   L.g = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pg * M * L.ldg * 2));
   L.dxp = reinterpret_cast<float*>(take((size_t)L.pieces * L.dx_split * M * d * 4));
@@ -1350,6 +1353,8 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
     MMF_TRY(encode_3d(&weighed, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.xw, a.d, L.m_pad, 2, (uint64_t)a.d * 2,
                       (uint64_t)L.m_pad * a.d * 2, hl::BK, 64));
   const CUtensorMap rows = P.x;
+  P.few_n = L.few_n;
+  P.dx_part = L.dxp;
   P.dx_split = dx ? L.dx_split : 0;
   P.dt_split = dtable ? L.dt_split : 0;
   const uint64_t f32row = (uint64_t)a.d * 4, trow = (uint64_t)a.d * dsize(a.tdt);
