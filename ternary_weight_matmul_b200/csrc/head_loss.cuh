@@ -88,7 +88,8 @@ struct Params {
   CUtensorMap g_out;   // the same array, box 64 x 32 (stores)
   CUtensorMap dx_out;  // float32 partials [planes][m_pad][d], box 32 x 32
   CUtensorMap dt_out;  // dtable's rows of the piece (its dtype), or float32 partials [planes][vocab][d]
-  const int32_t* live;  // device: live rows
+  const int32_t* live;  // device: live rows; nullptr: rows of the caller's x, taken as they are (kStats)
+  int32_t rows;
   int32_t d, vocab;
   int32_t v0, vn;       // vocabulary range of this launch
   int64_t m_pad;
@@ -448,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   dependency_wait();
-  const int live = *P.live;
+  const int live = P.live ? *P.live : P.rows;
   const Geo G = geometry<MODE>(P, live);
   const int tiles = G.tiles;
   const int live64 = (live + 63) & ~63;
@@ -469,7 +470,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
             const int k = (T.kb0 + kb) * BK;
             const uint32_t bar = in_first_cta(&full[s]);
             const int b_boxes = MODE == kProducts && T.n <= 128 ? 1 : B_BOXES;
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (A_BOXES + b_boxes) * BOX_BYTES);
+            // kStats reads nothing of the rows past the last: boxes of such rows are left out (a row of A
+            // reaches its own row of D only)
+            int a_boxes = A_BOXES, a_both = 2 * A_BOXES;
+            if (MODE == kStats) {
+              const int left = live - T.row;
+              a_both = left >= BM ? 2 * A_BOXES : (left + 63) >> 6;
+              a_boxes = min(max(a_both - A_BOXES * (int)rank, 0), A_BOXES);
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], (a_both + 2 * b_boxes) * BOX_BYTES);
             const int arow = T.row + CM * (int)rank, bcol = T.col + T.n / 2 * (int)rank;
             if (MODE == kProducts && T.kind == 2) {  // A MN-major, B K-major, k = vocabulary
 #pragma unroll
@@ -477,7 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
               for (int i = 0; i < b_boxes; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.g, k, bcol + 64 * i, pa, bar);
             } else if (MODE != kProducts) {
 #pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, arow + 64 * i, pa, bar);
+              for (int i = 0; i < A_BOXES; ++i)
+                if (i < a_boxes) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, arow + 64 * i, pa, bar);
 #pragma unroll
               for (int i = 0; i < B_BOXES; ++i)
                 tma_load_3d(sb + i * BOX_BYTES, &P.t, k, P.v0 + bcol + 64 * i, pb, bar);
@@ -622,12 +632,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           for (int e = 0; e < W; ++e)
             if (e >= left) sum[e] = -INFINITY;
         }
-        const int tgt = P.tgt && row < live ? P.tgt[row] - P.v0 - col0 : -1;
-        if ((uint32_t)tgt < (uint32_t)W) {
+        const uint32_t tgt = P.tgt && row < live ? (uint32_t)P.tgt[row] - (uint32_t)(P.v0 + col0) : 0xffffffffu;
+        if (tgt < (uint32_t)W) {
           float hit = 0.0f;
 #pragma unroll
           for (int e = 0; e < W; ++e)
-            if (tgt == e) hit = sum[e];
+            if (tgt == (uint32_t)e) hit = sum[e];
           P.st[row] = hit * unit;
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -646,7 +656,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           int64_t base = 0;
           int2 ent = make_int2(0x7fffffff, 0);
           if (row < live) {
-            const int32_t r = P.rowmap[row];
+            const int32_t r = P.rowmap ? P.rowmap[row] : row;
             base = (int64_t)r * P.top_k;
             pos = P.top_start[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + r];
             if (pos < P.top_k) ent = P.top[base + pos];
@@ -1134,18 +1144,19 @@ __global__ void __launch_bounds__(kRowThreads) weigh_rows_kernel(const GatherArg
 // joining the tiles' statistics
 // ---------------------------------------------------------------------------------------------
 // lse_i = top / tau + log sum_j S_j exp((M_j - top) / tau) over the row's parts, and for the cross
-// entropy loss_i = lse_i - s_target / tau. CTA = 32 rows x 32 lanes over the parts, four parts in flight
+// entropy loss_i = lse_i - s_target / tau. Without live_p and rowmap every row of R is there, and those
+// that are not live get zeros. CTA = 32 rows x 32 lanes over the parts, four parts in flight
 // per lane (a lane's chain over 250 / 32 parts is what the call costs when there are few rows).
 constexpr int kJoinThreads = 1024;
 __global__ void __launch_bounds__(kJoinThreads) join_stats_kernel(const float2* __restrict__ part, int parts,
                                                                   int64_t m_pad, const int32_t* __restrict__ live_p,
-                                                                  const int32_t* __restrict__ rowmap,
+                                                                  const int32_t* __restrict__ rowmap, const Rows R,
                                                                   const float* __restrict__ st, float inv_tau,
                                                                   float* loss, float* lse_out) {
   dependent();
   __shared__ float2 red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int live = *live_p;
+  const int live = live_p ? *live_p : R.m;
   const int64_t i = (int64_t)blockIdx.x * 32 + tx;
   if ((int64_t)blockIdx.x * 32 >= live) return;
   float mx = -INFINITY, sum = 0.0f;
@@ -1172,10 +1183,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_stats_kernel(const float2* 
   const float s = warp_sum(p.y * expf((p.x - ref) * inv_tau));
   const int64_t row = (int64_t)blockIdx.x * 32 + ty;
   if (tx == 0 && row < live) {
-    const float l = top * inv_tau + logf(s);
-    const int64_t r = rowmap[row];
+    const bool is = rowmap || row_live(R, (int)row);
+    const float l = is ? top * inv_tau + logf(s) : 0.0f;
+    const int64_t r = rowmap ? rowmap[row] : row;
     lse_out[r] = l;
-    if (st) loss[r] = l - st[row] * inv_tau;
+    if (st || !is) loss[r] = is ? l - st[row] * inv_tau : 0.0f;
   }
 }
 

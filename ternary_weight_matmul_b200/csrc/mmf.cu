@@ -1067,6 +1067,7 @@ struct LossPlan {
   int32_t px, pt, pg;       // planes of x, the table and g
   int gp;                   // hl::GradPlanes
   int32_t few_n;            // rows as N of dx's tiles, or 0
+  bool in_place;            // forward: the caller's rows as they are
   int32_t parts;            // statistics parts per row
   int64_t piece, ldg;       // vocabulary columns per piece, row pitch of g
   int32_t pieces, dx_split, dt_split;
@@ -1130,6 +1131,9 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   }
   L.tgt = reinterpret_cast<int32_t*>(take(M * 4));
   if (!backward) {
+    // One row tile of bf16: leaving rows out saves no work, so they stay where they are (a row's statistics
+    // meet no other row) and the gather's launch is saved.
+    L.in_place = m <= hl::BM && L.px == 1 && !tf32;
     L.parts = (int32_t)(2 * cdiv64(vocab, hl::BN));
     L.part = reinterpret_cast<float2*>(take((size_t)L.parts * M * sizeof(float2)));
     L.st = reinterpret_cast<float*>(take(M * 4));
@@ -1202,16 +1206,21 @@ mmf_status check_loss(const LossArgs& a, const char* name, bool distill, int32_t
   return MMF_OK;
 }
 
-// The launches before the products: live rows, gathered rows, table planes. Fills the parts of P
-// that every product launch shares. s_top: the forward's output, or nullptr.
-mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, float* s_top, hl::Params& P,
-                     const DevInfo& di, cudaStream_t st, int* launches) {
-  const unsigned row_ctas = (unsigned)(L.m_pad / (hl::kRowThreads / 32));
+hl::Rows loss_row_set(const LossArgs& a, const LossPlan& L) {
   hl::Rows R;
   R.targets = a.targets;
   R.flags = L.flags;
   R.vocab = a.vocab;
   R.m = (int32_t)a.m;
+  return R;
+}
+
+// The launches before the products: live rows, gathered rows, table planes. Fills the parts of P
+// that every product launch shares. s_top: the forward's output, or nullptr.
+mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, float* s_top, hl::Params& P,
+                     const DevInfo& di, cudaStream_t st, int* launches) {
+  const unsigned row_ctas = (unsigned)(L.m_pad / (hl::kRowThreads / 32));
+  const hl::Rows R = loss_row_set(a, L);
   if (!a.targets) {
     launch_after(hl::teacher_rows_kernel, dim3((unsigned)(L.m_pad / hl::kTeacherRows)), dim3(hl::kTeacherRows * 32), 0, st,
              a.teacher, a.m, L.m_pad, L.parts, L.flags, L.top, L.top_start, s_top, L.q);
@@ -1227,7 +1236,9 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   ga.x_unit = L.x_unit;
   ga.row_most = L.row_most;
   const dim3 grid(row_ctas), block(hl::kRowThreads);
-  if (a.m <= hl::kOneLaunchRows) {
+  if (L.in_place) {
+    // nothing to gather
+  } else if (a.m <= hl::kOneLaunchRows) {
     if (a.xdt == MMF_F32) launch_after(hl::place_rows_kernel<MMF_F32>, grid, block, 0, st, ga, L.rowmap, L.live);
     else launch_after(hl::place_rows_kernel<MMF_BF16>, grid, block, 0, st, ga, L.rowmap, L.live);
     ++*launches;
@@ -1260,9 +1271,13 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   }
   MMF_TRY(check_launch("head loss row kernels"));
   const uint64_t row = (uint64_t)a.d * 2;
-  MMF_TRY(encode_3d(&P.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.xg, a.d, L.m_pad, L.px, row, L.m_pad * row, hl::BK, 64));
+  if (L.in_place)
+    MMF_TRY(encode_3d(&P.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.d, a.m, 1, row, a.m * row, hl::BK, 64));
+  else
+    MMF_TRY(encode_3d(&P.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.xg, a.d, L.m_pad, L.px, row, L.m_pad * row, hl::BK, 64));
   MMF_TRY(encode_3d(&P.t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, table, a.d, a.vocab, L.pt, row, a.vocab * row, hl::BK, 64));
-  P.live = L.live;
+  P.live = L.in_place ? nullptr : L.live;
+  P.rows = (int32_t)a.m;
   P.d = a.d;
   P.vocab = a.vocab;
   P.m_pad = L.m_pad;
@@ -1297,17 +1312,16 @@ mmf_status loss_forward(const LossArgs& a, float* loss, float* lse, float* s_top
   P.vn = a.vocab;
   P.part = L.part;
   P.st = L.st;
-  P.tgt = ga.tgt;
+  P.tgt = L.in_place ? a.targets : ga.tgt;
   P.top = L.top;
   P.top_start = L.top_start;
-  P.rowmap = L.rowmap;
+  P.rowmap = L.in_place ? nullptr : L.rowmap;
   P.s_top = s_top;
   P.top_k = a.teacher.k;
   if (L.px == 1 && L.pt == 1) loss_launch<hl::kStats, 1>(P, *di, st);
   else loss_launch<hl::kStats, 2>(P, *di, st);
   launch_after(hl::join_stats_kernel, dim3((unsigned)(L.m_pad / 32)), dim3(hl::kJoinThreads), 0, st, (const float2*)L.part, L.parts,
-           L.m_pad, (const int32_t*)L.live, (const int32_t*)L.rowmap, a.targets ? (const float*)L.st : nullptr,
-           1.0f / a.tau, loss, lse);
+           L.m_pad, P.live, P.rowmap, loss_row_set(a, L), a.targets ? (const float*)L.st : nullptr, 1.0f / a.tau, loss, lse);
   launches += 2;
   if (!a.targets) {
     launch_after(hl::distill_loss_kernel, dim3((unsigned)(L.m_pad / (hl::kRowThreads / 32))), dim3(hl::kRowThreads), 0, st,
