@@ -288,7 +288,7 @@ mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t 
 /* Its gradients: u = dy norm_w, dx = rho u - rho^3 x mean(u x), dnorm_w[c] = sum_r dy[r][c] x[r][c] rho_r.
  *   x [m][d] x_dtype; dy [m][d] dy_dtype; dx [m][d] x_dtype out; dnorm_w [d] float32 out or NULL.
  *   ws >= mmf_workspace_bytes(MMF_OP_RMSNORM_BWD, m, d, 0, 0) when dnorm_w is asked for.
- * Float32 sums in a fixed order (deterministic). m = 0 writes a zero dnorm_w. */
+ * Float32 sums in a fixed order (deterministic). m = 0 writes a zero dnorm_w. dx may not alias an input. */
 mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
                                 const void* dy, mmf_dtype dy_dtype, void* dx, float* dnorm_w, void* ws,
                                 size_t ws_bytes, mmf_stream_t stream);
@@ -302,9 +302,10 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
  *           that row is computed with (it may hold anything).
  *   loss, lse [m] float32 out. Sums and mean over the rows are the caller's.
  *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, n_layers as at mmf_op). m = 0 is a no-op.
- * bf16 tensor cores with float32 accumulation and softmax statistics; a float32 operand enters as
- * three bf16 planes that hold it exactly, so float32 inputs give float32-accurate results.
- * Deterministic. */
+ * Tensor cores with float32 accumulation (in short runs that are added rounding to nearest) and float32
+ * softmax statistics. float32 operands enter as sums of 16-bit values (x beside a bf16 table as three bf16
+ * values, exactly; with a float32 table both as two fp16 values under a power of two, to 2^-22), so the
+ * results are those of float32 arithmetic. Deterministic; no output may alias an input. */
 mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                 mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, float* loss, float* lse,
                                 void* ws, size_t ws_bytes, mmf_stream_t stream);
@@ -314,8 +315,10 @@ mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int
  *   dx = g table          [m][d] x_dtype out or NULL, 16-byte aligned (zero in rows left out)
  *   dtable = g^T x        [vocab][d] table_dtype out or NULL, 16-byte aligned (every row written)
  * The logits are computed again in pieces of the vocabulary; one piece's g is held in the workspace
- * (about 512 MB at most up to 65536 rows). g is rounded to bf16 once where x and table are bf16, and
- * kept as three exact planes otherwise; both products accumulate in float32.
+ * (about 512 MB at most up to 65536 rows). g is rounded to bf16 once where x and table are bf16 (held in
+ * two bf16 values up to 128 rows); with float32 rows beside a bf16 table it is kept exactly, and with a
+ * float32 table g / dloss to 2^-22, or 2^-39 where it is below 2^-17. Products accumulate in float32.
+ * Deterministic; no output may alias an input.
  *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, n_layers as at mmf_op). m = 0 zeroes dtable. */
 mmf_status mmf_lm_head_xent_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                      mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, const float* lse,
@@ -340,7 +343,7 @@ mmf_status mmf_lm_head_distill_fwd(const void* x, mmf_dtype x_dtype, int64_t m, 
 
 /* Its gradients: g_rv = dloss[r] / temperature (exp(s_rv / temperature - lse[r]) - sum_{j: id = v} q_rj),
  * dx = g table, dtable = g^T x as above (the teacher's entries are computed whole in float32 before
- * their one rounding).  ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, n_layers as at mmf_op). */
+ * any rounding).  ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, n_layers as at mmf_op). */
 mmf_status mmf_lm_head_distill_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                         mmf_dtype table_dtype, int32_t vocab, const int32_t* t_ids,
                                         const void* t_logits, mmf_dtype t_dtype, int32_t top_k, float temperature,
