@@ -1446,9 +1446,9 @@ RmsPlan rms_plan(int32_t d, std::initializer_list<const void*> ptrs) {
 template <mmf_dtype XT, mmf_dtype YT>
 void rms_fwd_launch(const rms::Args& a, const RmsPlan& p, const DevInfo& di, cudaStream_t st) {
   const auto grid = [&](int rows) { return dim3((unsigned)std::min<int64_t>((a.m + rows - 1) / rows, (int64_t)di.sms * 16)); };
-  if (p.chunks == 1) launch_k(rms::rms_fwd_kernel<XT, YT, 1, 2>, grid(2), dim3(p.threads), 0, st, a);
-  else if (p.chunks == 2) launch_k(rms::rms_fwd_kernel<XT, YT, 2, 1>, grid(1), dim3(p.threads), 0, st, a);
-  else launch_k(rms::rms_fwd_kernel<XT, YT, 4, 1>, grid(1), dim3(p.threads), 0, st, a);
+  if (p.chunks == 1) launch_after(rms::rms_fwd_kernel<XT, YT, 1, 2>, grid(2), dim3(p.threads), 0, st, a);
+  else if (p.chunks == 2) launch_after(rms::rms_fwd_kernel<XT, YT, 2, 1>, grid(1), dim3(p.threads), 0, st, a);
+  else launch_after(rms::rms_fwd_kernel<XT, YT, 4, 1>, grid(1), dim3(p.threads), 0, st, a);
 }
 // rows per turn of the backward: as many as keep the raw chunks of two turns in registers
 template <mmf_dtype XT, mmf_dtype GT>
@@ -1456,9 +1456,9 @@ constexpr int kRmsRows = XT == MMF_BF16 && GT == MMF_BF16 ? 3 : 2;
 template <mmf_dtype XT, mmf_dtype GT>
 void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t st) {
   const dim3 grid((unsigned)ctas);
-  if (p.chunks == 1) launch_k(rms::rms_bwd_kernel<XT, GT, 1, kRmsRows<XT, GT>>, grid, dim3(p.threads), 0, st, a);
-  else if (p.chunks == 2) launch_k(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
-  else launch_k(rms::rms_bwd_kernel<XT, GT, 4, 1>, grid, dim3(p.threads), 0, st, a);
+  if (p.chunks == 1) launch_after(rms::rms_bwd_kernel<XT, GT, 1, kRmsRows<XT, GT>>, grid, dim3(p.threads), 0, st, a);
+  else if (p.chunks == 2) launch_after(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
+  else launch_after(rms::rms_bwd_kernel<XT, GT, 4, 1>, grid, dim3(p.threads), 0, st, a);
 }
 
 }  // namespace
@@ -2434,7 +2434,7 @@ mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t 
   LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (dsize(x_dtype) + dsize(y_dtype)), st);
   const RmsPlan p = rms_plan(d, {x, y, norm_w});
   if (!p.vec) {
-    launch_k(rms::rms_fwd_any_kernel, dim3((unsigned)std::min<int64_t>(m, (int64_t)di->sms * 8)), dim3(rms::kGenThreads), 0, st, a);
+    launch_after(rms::rms_fwd_any_kernel, dim3((unsigned)std::min<int64_t>(m, (int64_t)di->sms * 8)), dim3(rms::kGenThreads), 0, st, a);
   } else if (x_dtype == MMF_F32) {
     if (y_dtype == MMF_F32) rms_fwd_launch<MMF_F32, MMF_F32>(a, p, *di, st);
     else rms_fwd_launch<MMF_F32, MMF_BF16>(a, p, *di, st);
@@ -2470,7 +2470,7 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
   const int rows = !p.vec || p.chunks != 1 ? 1 : x_dtype == MMF_BF16 && dy_dtype == MMF_BF16 ? 3 : 2;
   const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * 4, kRmsMaxParts});
   if (!p.vec) {
-    launch_k(rms::rms_bwd_any_kernel, dim3((unsigned)ctas), dim3(rms::kGenThreads), 0, st, a);
+    launch_after(rms::rms_bwd_any_kernel, dim3((unsigned)ctas), dim3(rms::kGenThreads), 0, st, a);
   } else if (x_dtype == MMF_F32) {
     if (dy_dtype == MMF_F32) rms_bwd_launch<MMF_F32, MMF_F32>(a, p, ctas, st);
     else rms_bwd_launch<MMF_F32, MMF_BF16>(a, p, ctas, st);
@@ -2479,7 +2479,7 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
     else rms_bwd_launch<MMF_BF16, MMF_BF16>(a, p, ctas, st);
   }
   if (dnorm_w) {
-    launch_k(rms::rms_dw_kernel, dim3((unsigned)((d + 31) / 32)), dim3(1024), 0, st, (const float*)a.part, ctas, d, dnorm_w);
+    launch_after(rms::rms_dw_kernel, dim3((unsigned)((d + 31) / 32)), dim3(1024), 0, st, (const float*)a.part, ctas, d, dnorm_w);
     g_launches.fetch_add(1);  // two kernels under one timing scope
   }
   return check_launch("rmsnorm backward kernels");

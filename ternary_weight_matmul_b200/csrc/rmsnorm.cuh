@@ -33,6 +33,13 @@ struct Args {
   float eps;
 };
 
+// These kernels launch as programmatic dependents: set-up overlaps the end of the kernel before, nothing
+// is read or written before the wait.
+__device__ __forceinline__ void dependent() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <mmf_dtype DT>
 __device__ __forceinline__ void load8(const void* p, int64_t idx, float (&v)[8]) {
   if (DT == MMF_F32) {
@@ -90,6 +97,7 @@ __device__ __forceinline__ void block_sums(float (&v)[V], float (*red)[16]) {
 // d % 8 == 0, 16-byte aligned rows; chunk j of thread t is j * blockDim.x + t.
 template <mmf_dtype XT, mmf_dtype YT, int NC, int R>
 __global__ void __launch_bounds__(kMaxThreads) rms_fwd_kernel(const Args a) {
+  dependent();
   __shared__ float red[2][R][16];
   const int nck = a.d >> 3, T = blockDim.x;
   const float inv_d = 1.0f / (float)a.d;
@@ -160,6 +168,7 @@ __device__ __forceinline__ float raw_at(const Raw8<DT>& r, int e) {
 // across its barrier.
 template <mmf_dtype XT, mmf_dtype GT, int NC, int R>
 __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
+  dependent();
   __shared__ float red[2][2 * R][16];
   const int nck = a.d >> 3, T = blockDim.x;
   const float inv_d = 1.0f / (float)a.d;
@@ -240,6 +249,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
 
 // Any width and alignment: a CTA walks its rows one at a time, elements through memory twice.
 __global__ void __launch_bounds__(kGenThreads) rms_fwd_any_kernel(const Args a) {
+  dependent();
   __shared__ float red[32];
   for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
     float ss = 0.0f;
@@ -253,6 +263,7 @@ __global__ void __launch_bounds__(kGenThreads) rms_fwd_any_kernel(const Args a) 
   }
 }
 __global__ void __launch_bounds__(kGenThreads) rms_bwd_any_kernel(const Args a) {
+  dependent();
   __shared__ float red[32];
   float* part = a.part ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
   if (part)
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(kGenThreads) rms_bwd_any_kernel(const Args a) 
 
 // dw[c] = sum over the partial rows, in a fixed order: 32 columns x 32 lanes per CTA.
 __global__ void __launch_bounds__(1024) rms_dw_kernel(const float* __restrict__ part, int rows, int d, float* __restrict__ dw) {
+  dependent();
   __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
   float s = 0.0f;
