@@ -260,11 +260,11 @@ __device__ __forceinline__ uint32_t peel_half2(float& a, float& b) {
   b -= f.y;
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 2^k that brings `most`, the largest finite magnitude, to [2^14, 2^15); within what a float32 holds.
+// 2^k that brings `most`, the largest finite magnitude, to [2^14, 2^15); 2^126 at most, the largest whose
+// reciprocal is normal (below 2^-112 it falls short of 2^14).
 __device__ __forceinline__ float unit_up(float most) {
-  int e = (int)(__float_as_uint(most) >> 23) - 127;  // floor(log2); -127 for zero and subnormals
-  int k = 14 - e;
-  k = k < -110 ? -110 : k > 110 ? 110 : k;
+  const int e = (int)(__float_as_uint(most) >> 23) - 127;  // floor(log2); -127 for zero and subnormals
+  const int k = 14 - e > 126 ? 126 : 14 - e;               // -113 at least
   return most > 0.0f ? __uint_as_float((uint32_t)(127 + k) << 23) : 1.0f;
 }
 __device__ __forceinline__ float finite_abs(float v) {

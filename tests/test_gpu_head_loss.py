@@ -189,14 +189,14 @@ def test_xent_several_vocabulary_pieces(mmf, xt, tt, m, v):
 
 @pytest.mark.parametrize("xt,tt", TYPES[:2], ids=IDS[:2])
 @pytest.mark.parametrize("pattern", ["none", "one", "last", "alternate", "out of range"])
-@pytest.mark.parametrize("m", [515, 1030, 5001])
+@pytest.mark.parametrize("m", [101, 515, 1030, 5001])
 def test_xent_rows_left_out(mmf, m, xt, tt, pattern):
     d, v = 128, 700
     x, t, g = operands(11, m, d, v, xt, tt)
     targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
     drop = torch.ones(m, dtype=torch.bool, device=DEV)
     if pattern == "one":
-        drop[300] = False
+        drop[m // 2] = False
     elif pattern == "last":
         drop[-3:] = False
     elif pattern == "alternate":
@@ -253,7 +253,7 @@ def test_xent_large_logits_and_nan_stay_in_their_rows(mmf, m):
 
 
 @pytest.mark.parametrize("m", [90, 900])
-@pytest.mark.parametrize("up", [1e18, 1e-18])
+@pytest.mark.parametrize("up", [1e18, 1e-18, 1e30, 1e-30])
 def test_xent_float32_magnitudes(mmf, m, up):
     """Operands far from one with logits of order one: the fp16 pairs' powers of two at work."""
     x, t, g = operands(14, m, 128, 600, F32, F32)
@@ -261,6 +261,36 @@ def test_xent_float32_magnitudes(mmf, m, up):
     targets = torch.randint(0, 600, (m,), generator=g, device=DEV).to(torch.int32)
     check_xent(mmf, x * up, t / up, targets, torch.randn(m, generator=g, device=DEV))
     check_xent(mmf, x, t, targets, torch.randn(m, generator=g, device=DEV) * up)
+
+
+def test_offsets_past_32_bits(mmf):
+    """2.2 M rows of 1024: the last rows' elements lie past 2^31. Their results equal those of a call that
+    has only them (the same tiles' arithmetic; sums of dtable are left to the smaller tests)."""
+    m, d, v, tail = 2_200_000, 1024, 257, 512
+    assert (m - tail) * d > 2 ** 31
+    g = gen(15)
+    x = torch.empty(m, d, dtype=BF16, device=DEV)
+    x[:-tail] = 0.01
+    x[-tail:] = torch.randn(tail, d, generator=g, device=DEV).to(BF16)
+    t = (torch.randn(v, d, generator=g, device=DEV) / 16).to(BF16)
+    w = torch.rand(d, generator=g, device=DEV)
+    targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
+    targets[1::2] = -1                       # every other row is left out
+    last = slice(m - tail, m)
+    y, y_tail = mmf.rmsnorm_fwd(x, w), mmf.rmsnorm_fwd(x[last].contiguous(), w)
+    assert torch.equal(y[last], y_tail)
+    loss, lse = mmf.lm_head_xent_fwd(y, t, targets)
+    loss_tail, lse_tail = mmf.lm_head_xent_fwd(y_tail, t, targets[last].contiguous())
+    assert torch.equal(loss[last], loss_tail) and torch.equal(lse[last], lse_tail)
+    one = torch.ones(m, device=DEV)
+    dy, _ = mmf.lm_head_xent_backward(y, t, targets, lse, one, want_dtable=False)
+    del y
+    dy_tail, _ = mmf.lm_head_xent_backward(y_tail, t, targets[last].contiguous(), lse_tail, one[:tail], want_dtable=False)
+    assert torch.equal(dy[last], dy_tail)
+    dx, _ = mmf.rmsnorm_backward(x, w, dy)
+    dx_tail, _ = mmf.rmsnorm_backward(x[last].contiguous(), w, dy_tail)
+    assert torch.equal(dx[last], dx_tail)
+    assert mmf.sync_status(DEV) == mmf.MMF_OK
 
 
 def teacher_ref(ids, logits, v, tau):
@@ -327,7 +357,7 @@ def test_distill_several_vocabulary_pieces(mmf):
 
 
 @pytest.mark.parametrize("lt", [F32, BF16])
-@pytest.mark.parametrize("m", [260, 1000])
+@pytest.mark.parametrize("m", [60, 260, 1000])
 def test_distill_masked_entries(mmf, m, lt):
     d, v, k = 64, 500, 40
     x, t, _ = operands(23, m, d, v, BF16, BF16)
