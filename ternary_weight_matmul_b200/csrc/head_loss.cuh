@@ -25,7 +25,7 @@
 // With a float32 table everything is fp16 in two planes instead, hi = fp16(v 2^k), lo = fp16(v 2^k -
 // hi): 11 + 11 bits rounded to nearest, within 2^-22 of v, so three pairs (i + j <= 1; what they drop is
 // 2^-22 too) do what six do in bf16. The power of two keeps fp16's range: one per row for x (taken out
-// in the epilogue), one for the table, one for c x (c = dloss / tau), which is the rows' side of dT, and
+// in the epilogue), one for the table (the forward: one per row of it), one for c x (c = dloss / tau), which is the rows' side of dT, and
 // 2^15 for g / c = p - teacher, which lies in [-1, 1]. Values below 2^-17 of such a maximum lose bits
 // one by one down to steps of 2^-39 of it: less than float32's rounding of the sums they enter, though
 // not of a single p far below 2^-17.
@@ -119,7 +119,8 @@ struct Params {
   int32_t dt_f32;               // dt_out holds float32
   // float32 tables (fp16 planes): the powers of two to take out, else nullptr
   const float* x_unit;          // [m_pad] of each row of x
-  const float* t_unit;          // of the table
+  const float* t_unit;          // of the table (backward)
+  const float* t_units;         // [vocab] of each row of the table (forward)
   const float* dt_unit;         // of c x
   int32_t dt_row0;              // first row of dt_out this launch writes
   // kProducts with few rows: dx^T = T^T g^T, so that M is 256 columns of d and N the rows, in 64s; with
@@ -532,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
     if (lane == 0 && rank == 0) {
       // kind::f16: D float32 (bits 4-5 = 1), A and B bf16 or fp16 (bits 7-9, 10-12), MN-major A / B at
       // bits 15 / 16, N >> 3 at bits 17-22, M >> 4 at bits 24-28
-      const uint32_t fmt = P.t_unit ? 0u : 1u;  // fp16 : bf16
+      const uint32_t fmt = P.x_unit ? 0u : 1u;  // fp16 : bf16
       const uint32_t idesc0 = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(BM >> 4) << 24);
       uint32_t it = 0, n = 0;
       bool ok = true;
@@ -619,10 +620,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
       // the powers of two of fp16 operands: of the row and the table, or of dT's (dx's go where its
       // partials are added)
       float unit = 1.0f;
-      if (FLUSH && P.t_unit)
-        unit = MODE != kProducts ? (row < live ? P.x_unit[row] * *P.t_unit : 0.0f)
-               : T.kind == 0     ? *P.dt_unit * (1.0f / kGradUnit)
-                                 : 1.0f;
+      if (FLUSH && P.x_unit)
+        unit = MODE == kStats   ? (row < live ? P.x_unit[row] : 0.0f)
+               : MODE == kGrad  ? (row < live ? P.x_unit[row] * *P.t_unit : 0.0f)
+               : T.kind == 0    ? *P.dt_unit * (1.0f / kGradUnit)
+                                : 1.0f;
+      if (MODE == kStats && GP > 1 && P.t_units) {
+        const float4* u4 = reinterpret_cast<const float4*>(P.t_units + col0);  // one address for the warp
+#pragma unroll
+        for (int e = 0; e < (FLUSH ? BN / 2 : 0); e += 4) {
+          const float4 u = u4[e / 4];
+          sum[e] *= u.x;
+          sum[e + 1] *= u.y;
+          sum[e + 2] *= u.z;
+          sum[e + 3] *= u.w;
+        }
+      }
       const float scale = P.scale * unit;
       // columns [c0, c0 + N) of D into v (with FLUSH they are in `sum` already)
       const auto cols32 = [&](int c0, float* v) {
@@ -1112,6 +1125,38 @@ __global__ void __launch_bounds__(kRowThreads) split_table_kernel(const float* _
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       reinterpret_cast<uint4*>(out + j * count)[e] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+  }
+}
+
+// float32 table -> two fp16 planes [2][rows][d], every row by its own power of two (unit[row] to take it
+// out again): the forward's, whose epilogue has a word per column; one pass over the table where a common
+// power takes two (the backward's, in which words are summed over). One warp per row.
+__global__ void __launch_bounds__(kRowThreads) split_rows_kernel(const float* __restrict__ t, int rows, int d,
+                                                                 __nv_bfloat16* __restrict__ out,
+                                                                 float* __restrict__ unit) {
+  dependent();
+  const int lane = threadIdx.x & 31, nck = d >> 3;
+  const int64_t count = (int64_t)rows * d;
+  for (int64_t r = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5); r < rows;
+       r += (int64_t)gridDim.x * (kRowThreads / 32)) {
+    float most = 0.0f, v[8];
+    for (int c = lane; c < nck; c += 32) {
+      load_row8<MMF_F32>(t, r * d + 8 * c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, finite_abs(v[e]));
+    }
+    const float up = unit_up(warp_max(most));
+    if (lane == 0) unit[r] = 1.0f / up;
+    for (int c = lane; c < nck; c += 32) {
+      uint32_t p[PLANES][4];
+      load_row8<MMF_F32>(t, r * d + 8 * c, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= up;
+      half_planes<2>(v, p);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        reinterpret_cast<uint4*>(out + j * count + r * d)[c] = make_uint4(p[j][0], p[j][1], p[j][2], p[j][3]);
+    }
   }
 }
 

@@ -1079,7 +1079,7 @@ struct LossPlan {
   __nv_bfloat16* tp;        // table planes
   __nv_bfloat16* xw;        // c x planes
   float* most;              // largest magnitudes of the table, per CTA
-  float* units;             // powers of two to take out: of the table, of c x
+  float* units;             // powers of two to take out: of the table, of c x (forward: of the table's rows)
   float* x_unit;            // ... of each row
   float* row_most;
   float2* part;
@@ -1121,8 +1121,12 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   L.xg = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.px * M * d * 2));
   if (tf32) {
     L.tp = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pt * vocab * d * 2));
-    L.most = reinterpret_cast<float*>(take(hl::kMostParts * sizeof(float)));
-    L.units = reinterpret_cast<float*>(take(2 * sizeof(float)));
+    if (backward) {
+      L.most = reinterpret_cast<float*>(take(hl::kMostParts * sizeof(float)));
+      L.units = reinterpret_cast<float*>(take(2 * sizeof(float)));
+    } else {
+      L.units = reinterpret_cast<float*>(take((size_t)cdiv64(vocab, hl::BN) * hl::BN * sizeof(float)));
+    }
     L.x_unit = reinterpret_cast<float*>(take(M * 4));
     if (backward) {
       L.xw = reinterpret_cast<__nv_bfloat16*>(take(2 * M * d * 2));
@@ -1249,22 +1253,25 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
     *launches += 2;
   }
   const void* table = a.table;
-  if (a.tdt == MMF_F32) {
-    const int64_t count = (int64_t)a.vocab * a.d;
-    const unsigned ctas = (unsigned)std::min<int64_t>((count / 8 + hl::kRowThreads - 1) / hl::kRowThreads, (int64_t)di.sms * 16);
-    const int parts = (int)std::min<unsigned>(ctas, hl::kMostParts);
-    launch_after(hl::table_most_kernel, dim3(parts), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
-                 count, L.most);
-    launch_after(hl::split_table_kernel, dim3(ctas), dim3(hl::kRowThreads), 0, st, reinterpret_cast<const float*>(a.table),
-                 count, (const float*)L.most, parts, L.tp, L.units);
-    *launches += 2;
+  const float* tf = reinterpret_cast<const float*>(a.table);
+  if (a.tdt == MMF_F32 && !L.most) {  // forward
+    const unsigned ctas = (unsigned)std::min<int64_t>(cdiv64(a.vocab, hl::kRowThreads / 32), (int64_t)di.sms * 8);
+    launch_after(hl::split_rows_kernel, dim3(ctas), block, 0, st, tf, a.vocab, a.d, L.tp, L.units);
+    ++*launches;
     table = L.tp;
-    if (L.xw) {
-      const unsigned wctas = (unsigned)std::min<int64_t>(row_ctas, (int64_t)di.sms * 8);
-      if (a.xdt == MMF_F32) launch_after(hl::weigh_rows_kernel<MMF_F32>, dim3(wctas), block, 0, st, ga, L.xw, L.units + 1);
-      else launch_after(hl::weigh_rows_kernel<MMF_BF16>, dim3(wctas), block, 0, st, ga, L.xw, L.units + 1);
-      ++*launches;
-    }
+    P.x_unit = L.x_unit;
+    P.t_units = L.units;
+  } else if (a.tdt == MMF_F32) {
+    const int64_t count = (int64_t)a.vocab * a.d;
+    const unsigned ctas = (unsigned)std::min<int64_t>(cdiv64(count / 8, hl::kRowThreads), (int64_t)di.sms * 16);
+    const int parts = (int)std::min<unsigned>(ctas, hl::kMostParts);
+    const unsigned wctas = (unsigned)std::min<int64_t>(row_ctas, (int64_t)di.sms * 8);
+    launch_after(hl::table_most_kernel, dim3(parts), block, 0, st, tf, count, L.most);
+    launch_after(hl::split_table_kernel, dim3(ctas), block, 0, st, tf, count, (const float*)L.most, parts, L.tp, L.units);
+    if (a.xdt == MMF_F32) launch_after(hl::weigh_rows_kernel<MMF_F32>, dim3(wctas), block, 0, st, ga, L.xw, L.units + 1);
+    else launch_after(hl::weigh_rows_kernel<MMF_BF16>, dim3(wctas), block, 0, st, ga, L.xw, L.units + 1);
+    *launches += 3;
+    table = L.tp;
     P.x_unit = L.x_unit;
     P.t_unit = L.units;
     P.dt_unit = L.units + 1;
