@@ -701,10 +701,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
       } else if (MODE == kGrad) {
         // pad rows have c = lse = 0: zeros, which dT's last k-block of rows relies on; past that nobody
         // reads what a row leaves
-        if (row0 < live64) {
+        const bool needed = row0 < live64;  // uniform across the warp
         constexpr bool halves = GP == kHalf2;
-        const float c = !halves ? P.c[row] : row < live ? kGradUnit : 0.0f, lse2 = P.lse[row] * kLog2e;
-        const int tgt = P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
+        const float c = !needed ? 0.0f : !halves ? P.c[row] : row < live ? kGradUnit : 0.0f;
+        const float lse2 = needed ? P.lse[row] * kLog2e : 0.0f;
+        const int tgt = needed && P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
         const auto grads = [&](float* gv, int c0, int w) {
 #pragma unroll
           for (int e = 0; e < w; ++e) gv[e] = ex2(fmaf(gv[e], scale, -lse2));
@@ -716,46 +717,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
           for (int e = 0; e < w; ++e) gv[e] *= c;
         };
-        if (FLUSH) grads(sum, 0, FLUSH ? BN / 2 : 0);
+        if (FLUSH && needed && grad_planes(GP) != 2) grads(sum, 0, FLUSH ? BN / 2 : 0);
 #pragma unroll
         for (int c0 = 0; c0 < BN / 2; c0 += 64) {
-          if (col0 + c0 >= P.vn) break;
+          if (!needed || col0 + c0 >= P.vn) break;
           float own[FLUSH ? 1 : 64];
           float* gv = FLUSH ? sum + (FLUSH ? c0 : 0) : own;
           if (!FLUSH) {
             cols32(c0, gv);
             cols32(c0 + 32, gv + 32);
-            grads(gv, c0, FLUSH ? 0 : 64);
+            if (grad_planes(GP) != 2) grads(gv, c0, FLUSH ? 0 : 64);
           }
-#pragma unroll
-          for (int p = 0; p < grad_planes(GP); ++p) {
-            if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
+          if (grad_planes(GP) == 2) {
+            // both planes at once, one per buffer: a value is worked out, split and gone
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              uint32_t w[4];
+              uint32_t hi[4], lo[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                float& a = gv[8 * j + 2 * q];
-                float& b = gv[8 * j + 2 * q + 1];
-                // keeps the compiler from splitting all values ahead of the stores, into spills
-                asm volatile("" : "+f"(a), "+f"(b));
-                if (GP == kFine2 && p == 0) w[q] = peel_bf16_rn(a, b);
-                else if (!FLUSH) w[q] = pack_bf16_rn(a, b);
-                else if (halves) w[q] = peel_half2(a, b);
-                else w[q] = pack_bf16_hi(peel(a), peel(b));
+                const int e = 8 * j + 2 * q;
+                float a = ex2(fmaf(gv[e], scale, -lse2)), b = ex2(fmaf(gv[e + 1], scale, -lse2));
+                if (tgt - c0 == e) a -= 1.0f;
+                if (tgt - c0 == e + 1) b -= 1.0f;
+                a *= c;
+                b *= c;
+                hi[q] = halves ? peel_half2(a, b) : peel_bf16_rn(a, b);
+                lo[q] = halves ? pack_half(a, b) : pack_bf16_rn(a, b);
               }
-              st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), w[0], w[1], w[2], w[3]);
+              const uint32_t at = lane * 128 + (((uint32_t)j << 4) ^ swz);
+              st_shared_v4(stg0 + at, hi[0], hi[1], hi[2], hi[3]);
+              st_shared_v4(stg0 + OUT_BYTES + at, lo[0], lo[1], lo[2], lo[3]);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&P.g_out, stg, col0 + c0, row0, p);
+              tma_store_3d(&P.g_out, stg0, col0 + c0, row0, 0);
+              tma_store_3d(&P.g_out, stg0 + OUT_BYTES, col0 + c0, row0, 1);
               bulk_commit();
             }
-            next_buffer();
+          } else {
+#pragma unroll
+            for (int p = 0; p < grad_planes(GP); ++p) {
+              if (lane == 0) bulk_wait_read<OUT_BUFS - 1>();
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  float& a = gv[8 * j + 2 * q];
+                  float& b = gv[8 * j + 2 * q + 1];
+                  // keeps the compiler from splitting all values ahead of the stores, into spills
+                  asm volatile("" : "+f"(a), "+f"(b));
+                  w[q] = !FLUSH ? pack_bf16_rn(a, b) : pack_bf16_hi(peel(a), peel(b));
+                }
+                st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), w[0], w[1], w[2], w[3]);
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_3d(&P.g_out, stg, col0 + c0, row0, p);
+                bulk_commit();
+              }
+              next_buffer();
+            }
           }
-        }
         }
       } else if (T.kind == 2) {
         // lane = column of d, column = row: a row's 32 values leave as 128 bytes
