@@ -1452,6 +1452,17 @@ RmsPlan rms_plan(int32_t d, std::initializer_list<const void*> ptrs) {
 
 template <mmf_dtype XT, mmf_dtype YT>
 void rms_fwd_launch(const rms::Args& a, const RmsPlan& p, const DevInfo& di, cudaStream_t st) {
+  if (!p.vec) {
+    const auto any = [&](auto kern, int per_sm) {
+      launch_after(kern, dim3((unsigned)std::min<int64_t>(a.m, (int64_t)di.sms * per_sm)), dim3(rms::kGenThreads), 0, st, a);
+    };
+    if (a.d <= 2 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 2>, 6);
+    else if (a.d <= 5 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 5>, 6);
+    else if (a.d <= 9 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 9>, 6);
+    else if (a.d <= 12 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 12>, 6);
+    else any(rms::rms_fwd_any_kernel<XT, YT, 0>, 8);
+    return;
+  }
   const auto grid = [&](int rows) { return dim3((unsigned)std::min<int64_t>((a.m + rows - 1) / rows, (int64_t)di.sms * 16)); };
   if (p.chunks == 1) launch_after(rms::rms_fwd_kernel<XT, YT, 1, 2>, grid(2), dim3(p.threads), 0, st, a);
   else if (p.chunks == 2) launch_after(rms::rms_fwd_kernel<XT, YT, 2, 1>, grid(1), dim3(p.threads), 0, st, a);
@@ -1463,6 +1474,15 @@ constexpr int kRmsRows = XT == MMF_BF16 && GT == MMF_BF16 ? 3 : 2;
 template <mmf_dtype XT, mmf_dtype GT>
 void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t st) {
   const dim3 grid((unsigned)ctas);
+  if (!p.vec) {
+    const auto any = [&](auto kern) { launch_after(kern, grid, dim3(rms::kGenThreads), 0, st, a); };
+    if (a.d <= 2 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 2>);
+    else if (a.d <= 5 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 5>);
+    else if (a.d <= 9 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 9>);
+    else if (a.d <= 12 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 12>);
+    else any(rms::rms_bwd_any_kernel<XT, GT, 0>);
+    return;
+  }
   if (p.chunks == 1) launch_after(rms::rms_bwd_kernel<XT, GT, 1, kRmsRows<XT, GT>>, grid, dim3(p.threads), 0, st, a);
   else if (p.chunks == 2) launch_after(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
   else launch_after(rms::rms_bwd_kernel<XT, GT, 4, 1>, grid, dim3(p.threads), 0, st, a);
@@ -2437,12 +2457,10 @@ mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   rms::Args a;
   memset(&a, 0, sizeof(a));
-  a.x = x; a.w = norm_w; a.out = y; a.xdt = x_dtype; a.odt = y_dtype; a.m = m; a.d = d; a.eps = eps;
+  a.x = x; a.w = norm_w; a.out = y; a.m = m; a.d = d; a.eps = eps;
   LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (dsize(x_dtype) + dsize(y_dtype)), st);
   const RmsPlan p = rms_plan(d, {x, y, norm_w});
-  if (!p.vec) {
-    launch_after(rms::rms_fwd_any_kernel, dim3((unsigned)std::min<int64_t>(m, (int64_t)di->sms * 8)), dim3(rms::kGenThreads), 0, st, a);
-  } else if (x_dtype == MMF_F32) {
+  if (x_dtype == MMF_F32) {
     if (y_dtype == MMF_F32) rms_fwd_launch<MMF_F32, MMF_F32>(a, p, *di, st);
     else rms_fwd_launch<MMF_F32, MMF_BF16>(a, p, *di, st);
   } else {
@@ -2471,14 +2489,12 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
   rms::Args a;
   memset(&a, 0, sizeof(a));
   a.x = x; a.dy = dy; a.w = norm_w; a.out = dx; a.part = dnorm_w ? reinterpret_cast<float*>(ws) : nullptr;
-  a.xdt = x_dtype; a.dydt = dy_dtype; a.odt = x_dtype; a.m = m; a.d = d; a.eps = eps;
+  a.m = m; a.d = d; a.eps = eps;
   LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (2.0 * dsize(x_dtype) + dsize(dy_dtype)), st);
   const RmsPlan p = rms_plan(d, {x, dy, dx, norm_w});
   const int rows = !p.vec || p.chunks != 1 ? 1 : x_dtype == MMF_BF16 && dy_dtype == MMF_BF16 ? 3 : 2;
-  const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * 4, kRmsMaxParts});
-  if (!p.vec) {
-    launch_after(rms::rms_bwd_any_kernel, dim3((unsigned)ctas), dim3(rms::kGenThreads), 0, st, a);
-  } else if (x_dtype == MMF_F32) {
+  const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * (p.vec ? 4 : 5), kRmsMaxParts});
+  if (x_dtype == MMF_F32) {
     if (dy_dtype == MMF_F32) rms_bwd_launch<MMF_F32, MMF_F32>(a, p, ctas, st);
     else rms_bwd_launch<MMF_F32, MMF_BF16>(a, p, ctas, st);
   } else {

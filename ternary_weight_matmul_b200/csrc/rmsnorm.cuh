@@ -27,7 +27,6 @@ struct Args {
   const float* w;       // [d] or nullptr (1)
   void* out;            // forward y, backward dx
   float* part;          // backward [gridDim.x][d] partial dw, or nullptr
-  mmf_dtype xdt, dydt, odt;  // read by the general kernels
   int64_t m;
   int32_t d;
   float eps;
@@ -73,6 +72,10 @@ __device__ __forceinline__ void store8(void* p, int64_t idx, const float (&v)[8]
     *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p) + idx) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
+
+// rho u - k x, with its roundings spelled out: the compiler may otherwise pick either product for the fused
+// one, here this and there that, and dx would depend on whether dw is asked for
+__device__ __forceinline__ float grad(float rho, float u, float k, float x) { return fmaf(-k, x, __fmul_rn(rho, u)); }
 
 // Block sums of V values at once; red has V * 16 floats. One barrier before the result; the caller
 // alternates between two red arrays, so that the next call's writes cannot meet this call's reads.
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
         for (int e = 0; e < 8; ++e) {
           const float xv = raw_at<XT>(x[r][j], e), gv = raw_at<GT>(g[r][j], e);
           dw[j][e] = fmaf(gv * rho, xv, dw[j][e]);
-          o[e] = rho * (gv * w[j][e]) - k * xv;
+          o[e] = grad(rho, gv * w[j][e], k, xv);
         }
         store8<XT>(a.out, (r0 + r) * a.d + 8 * c, o);
       }
@@ -247,42 +250,105 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
   }
 }
 
-// Any width and alignment: a CTA walks its rows one at a time, elements through memory twice.
-__global__ void __launch_bounds__(kGenThreads) rms_fwd_any_kernel(const Args a) {
+// Any width and alignment: single columns, thread t's at t + j * kGenThreads. NC > 0: rows of up to NC *
+// kGenThreads columns, a thread's columns of a row (and its share of dw) in registers, one row at a time
+// so that six CTAs share an SM; NC = 0: wider rows, read twice, dw in the thread's columns of the partial
+// row.
+template <mmf_dtype DT>
+__device__ __forceinline__ float at(const void* p, int64_t i) {
+  return Elem<DT>::load(reinterpret_cast<const typename Elem<DT>::T*>(p) + i);
+}
+template <mmf_dtype DT>
+__device__ __forceinline__ void put(void* p, int64_t i, float v) {
+  Elem<DT>::store(reinterpret_cast<typename Elem<DT>::T*>(p) + i, v);
+}
+template <mmf_dtype XT, mmf_dtype YT, int NC>
+__global__ void __launch_bounds__(kGenThreads, NC > 0 ? 6 : 1) rms_fwd_any_kernel(const Args a) {
   dependent();
-  __shared__ float red[32];
-  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
-    float ss = 0.0f;
-    for (int c = threadIdx.x; c < a.d; c += kGenThreads) {
-      const float v = load_as_float(a.x, r * a.d + c, a.xdt);
-      ss = fmaf(v, v, ss);
+  __shared__ float red[2][1][16];
+  const int tid = threadIdx.x;
+  const float inv_d = 1.0f / (float)a.d;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x, turn ^= 1) {
+    float ss[1] = {0.0f}, x[NC > 0 ? NC : 1];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = tid + j * kGenThreads;
+      x[j] = c < a.d ? at<XT>(a.x, r * a.d + c) : 0.0f;
     }
-    const float rho = rsqrtf(block_sum(ss, red) / (float)a.d + a.eps);
-    for (int c = threadIdx.x; c < a.d; c += kGenThreads)
-      store_from_float(a.out, r * a.d + c, a.odt, load_as_float(a.x, r * a.d + c, a.xdt) * rho * (a.w ? a.w[c] : 1.0f));
+#pragma unroll
+    for (int j = 0; j < NC; ++j) ss[0] = fmaf(x[j], x[j], ss[0]);
+    if (NC == 0)
+      for (int c = tid; c < a.d; c += kGenThreads) {
+        const float v = at<XT>(a.x, r * a.d + c);
+        ss[0] = fmaf(v, v, ss[0]);
+      }
+    block_sums<1>(ss, red[turn]);
+    const float rho = rsqrtf(ss[0] * inv_d + a.eps);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = tid + j * kGenThreads;
+      if (c < a.d) put<YT>(a.out, r * a.d + c, x[j] * rho * (a.w ? a.w[c] : 1.0f));
+    }
+    if (NC == 0)
+      for (int c = tid; c < a.d; c += kGenThreads)
+        put<YT>(a.out, r * a.d + c, at<XT>(a.x, r * a.d + c) * rho * (a.w ? a.w[c] : 1.0f));
   }
 }
-__global__ void __launch_bounds__(kGenThreads) rms_bwd_any_kernel(const Args a) {
+template <mmf_dtype XT, mmf_dtype GT, int NC>
+__global__ void __launch_bounds__(kGenThreads, NC > 9 ? 4 : NC > 0 ? 5 : 1) rms_bwd_any_kernel(const Args a) {
   dependent();
-  __shared__ float red[32];
+  __shared__ float red[2][2][16];
+  const int tid = threadIdx.x;
   float* part = a.part ? a.part + (int64_t)blockIdx.x * a.d : nullptr;
-  if (part)
-    for (int c = threadIdx.x; c < a.d; c += kGenThreads) part[c] = 0.0f;  // each thread only touches its own columns
-  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x) {
-    float ss = 0.0f, ux = 0.0f;
-    for (int c = threadIdx.x; c < a.d; c += kGenThreads) {
-      const float v = load_as_float(a.x, r * a.d + c, a.xdt);
-      const float u = load_as_float(a.dy, r * a.d + c, a.dydt) * (a.w ? a.w[c] : 1.0f);
-      ss = fmaf(v, v, ss);
-      ux = fmaf(u, v, ux);
+  float dw[NC > 0 ? NC : 1];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) dw[j] = 0.0f;
+  if (NC == 0 && part)
+    for (int c = tid; c < a.d; c += kGenThreads) part[c] = 0.0f;  // each thread only touches its own columns
+  const float inv_d = 1.0f / (float)a.d;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x, turn ^= 1) {
+    float s[2] = {0.0f, 0.0f}, x[NC > 0 ? NC : 1], g[NC > 0 ? NC : 1];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = tid + j * kGenThreads;
+      x[j] = c < a.d ? at<XT>(a.x, r * a.d + c) : 0.0f;
+      g[j] = c < a.d ? at<GT>(a.dy, r * a.d + c) : 0.0f;
     }
-    const float rho = rsqrtf(block_sum(ss, red) / (float)a.d + a.eps);
-    const float k = rho * rho * rho * (block_sum(ux, red) / (float)a.d);
-    for (int c = threadIdx.x; c < a.d; c += kGenThreads) {
-      const float v = load_as_float(a.x, r * a.d + c, a.xdt), g = load_as_float(a.dy, r * a.d + c, a.dydt);
-      if (part) part[c] = fmaf(g * rho, v, part[c]);
-      store_from_float(a.out, r * a.d + c, a.odt, rho * (g * (a.w ? a.w[c] : 1.0f)) - k * v);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = tid + j * kGenThreads;
+      s[0] = fmaf(x[j], x[j], s[0]);
+      s[1] = fmaf(g[j] * (a.w && c < a.d ? a.w[c] : 1.0f), x[j], s[1]);
     }
+    if (NC == 0)
+      for (int c = tid; c < a.d; c += kGenThreads) {
+        const float v = at<XT>(a.x, r * a.d + c);
+        const float u = at<GT>(a.dy, r * a.d + c) * (a.w ? a.w[c] : 1.0f);
+        s[0] = fmaf(v, v, s[0]);
+        s[1] = fmaf(u, v, s[1]);
+      }
+    block_sums<2>(s, red[turn]);
+    const float rho = rsqrtf(s[0] * inv_d + a.eps);
+    const float k = rho * rho * rho * (s[1] * inv_d);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = tid + j * kGenThreads;
+      dw[j] = fmaf(g[j] * rho, x[j], dw[j]);
+      if (c < a.d) put<XT>(a.out, r * a.d + c, grad(rho, g[j] * (a.w ? a.w[c] : 1.0f), k, x[j]));
+    }
+    if (NC == 0)
+      for (int c = tid; c < a.d; c += kGenThreads) {
+        const float v = at<XT>(a.x, r * a.d + c), u = at<GT>(a.dy, r * a.d + c);
+        if (part) part[c] = fmaf(u * rho, v, part[c]);
+        put<XT>(a.out, r * a.d + c, grad(rho, u * (a.w ? a.w[c] : 1.0f), k, v));
+      }
+  }
+  if (part) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (tid + j * kGenThreads < a.d) part[tid + j * kGenThreads] = dw[j];
   }
 }
 
