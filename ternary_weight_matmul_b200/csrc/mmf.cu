@@ -1433,7 +1433,8 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
 // ---------------------------------------------------------------------------------------------
 // RMSNorm
 // ---------------------------------------------------------------------------------------------
-constexpr int kRmsMaxParts = 1024;  // partial rows of the gain's gradient (CTAs of the backward)
+// Partial rows of the gain's gradient (CTAs of the backward): narrow rows take small CTAs, so more of them.
+int64_t rms_max_parts(int32_t d) { return d <= 512 ? 2048 : 1024; }
 
 // Rows per CTA turn, and the vector kernels' shape: threads x chunks cover d / 8.
 struct RmsPlan {
@@ -1468,9 +1469,13 @@ void rms_fwd_launch(const rms::Args& a, const RmsPlan& p, const DevInfo& di, cud
   else if (p.chunks == 2) launch_after(rms::rms_fwd_kernel<XT, YT, 2, 1>, grid(1), dim3(p.threads), 0, st, a);
   else launch_after(rms::rms_fwd_kernel<XT, YT, 4, 1>, grid(1), dim3(p.threads), 0, st, a);
 }
-// rows per turn of the backward: as many as keep the raw chunks of two turns in registers
-template <mmf_dtype XT, mmf_dtype GT>
-constexpr int kRmsRows = XT == MMF_BF16 && GT == MMF_BF16 ? 3 : 2;
+// Rows per turn of the backward: as many as keep two turns' raw chunks in registers with two CTAs or more
+// on an SM (forward + backward of 16384 x 1536 bf16, 192 threads: 74 us with two rows, 58 with one; of
+// 16384 x 1024, 128 threads: 37.5 with three).
+int rms_bwd_rows(const RmsPlan& p, bool bf16) {
+  if (!p.vec || p.chunks != 1 || p.threads > (bf16 ? 128 : 256)) return 1;
+  return bf16 ? 3 : 2;
+}
 template <mmf_dtype XT, mmf_dtype GT>
 void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t st) {
   const dim3 grid((unsigned)ctas);
@@ -1483,7 +1488,12 @@ void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t
     else any(rms::rms_bwd_any_kernel<XT, GT, 0>);
     return;
   }
-  if (p.chunks == 1) launch_after(rms::rms_bwd_kernel<XT, GT, 1, kRmsRows<XT, GT>>, grid, dim3(p.threads), 0, st, a);
+  if (p.chunks == 1) {
+    const int rows = rms_bwd_rows(p, XT == MMF_BF16 && GT == MMF_BF16);
+    if (rows == 3) launch_after(rms::rms_bwd_kernel<XT, GT, 1, 3>, grid, dim3(p.threads), 0, st, a);
+    else if (rows == 2) launch_after(rms::rms_bwd_kernel<XT, GT, 1, 2>, grid, dim3(p.threads), 0, st, a);
+    else launch_after(rms::rms_bwd_kernel<XT, GT, 1, 1>, grid, dim3(p.threads), 0, st, a);
+  }
   else if (p.chunks == 2) launch_after(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
   else launch_after(rms::rms_bwd_kernel<XT, GT, 4, 1>, grid, dim3(p.threads), 0, st, a);
 }
@@ -1569,7 +1579,7 @@ size_t mmf_workspace_bytes(mmf_op op, int64_t m, int32_t d, int32_t inner, int32
     case MMF_OP_HEAD:
       return inner > 0 ? head_ws_bytes(inner, d) : 0;
     case MMF_OP_RMSNORM_BWD:
-      return align256((size_t)kRmsMaxParts * d * sizeof(float));
+      return align256((size_t)rms_max_parts(d) * d * sizeof(float));
     case MMF_OP_HEAD_LOSS:
     case MMF_OP_HEAD_LOSS_BWD:
       return d > 0 && inner > 0 ? loss_plan(m, d, inner, (n_layers & 1) != 0, (n_layers & 2) != 0,
@@ -2492,8 +2502,9 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
   a.m = m; a.d = d; a.eps = eps;
   LaunchScope ls(MMF_KERNEL_OTHER, (double)m * d * (2.0 * dsize(x_dtype) + dsize(dy_dtype)), st);
   const RmsPlan p = rms_plan(d, {x, dy, dx, norm_w});
-  const int rows = !p.vec || p.chunks != 1 ? 1 : x_dtype == MMF_BF16 && dy_dtype == MMF_BF16 ? 3 : 2;
-  const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * (p.vec ? 4 : 5), kRmsMaxParts});
+  const int rows = rms_bwd_rows(p, x_dtype == MMF_BF16 && dy_dtype == MMF_BF16);
+  const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * (!p.vec ? 5 : p.threads <= 64 ? 12 : 4),
+                                           rms_max_parts(d)});
   if (x_dtype == MMF_F32) {
     if (dy_dtype == MMF_F32) rms_bwd_launch<MMF_F32, MMF_F32>(a, p, ctas, st);
     else rms_bwd_launch<MMF_F32, MMF_BF16>(a, p, ctas, st);
