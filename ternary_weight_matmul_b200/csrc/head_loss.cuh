@@ -38,8 +38,8 @@
 // error of the loss at d = 1024: 1.2e-6 without, 5.6e-7 with 8 k-blocks, 2.6e-7 with 4; of a float32
 // product 4e-7.)
 //
-// Measured (32000 words, bf16, back to back): 16384 x 1024 forward + backward 3.54 ms = 1154 TFLOP/s of
-// 8 m vocab d (5% of the rows left out), 0.84 of the sustained cuBLAS rate; 16384 x 2560 6.29 ms = 1195
+// Measured (32000 words, bf16, back to back): 16384 x 1024 forward + backward 3.53 ms = 1156 TFLOP/s of
+// 8 m vocab d (5% of the rows left out), 0.84 of the sustained cuBLAS rate; 16384 x 2560 6.26 ms = 1200
 // (0.87). Alone, 4096 x 1024: statistics 200 us (1340 TFLOP/s), g 204, products 382 (1405); the tensor
 // pipe is active 73 / 71 / 79% of the cycles at 1.6 GHz, TMA loads 10.3 to 11 TB/s out of the L2. What
 // bounds it: shared memory, whose 128 bytes a cycle the MMA's operand reads (64) and the TMA's writes (64)

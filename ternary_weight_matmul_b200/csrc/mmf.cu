@@ -1460,7 +1460,7 @@ void rms_fwd_launch(const rms::Args& a, const RmsPlan& p, const DevInfo& di, cud
     if (a.d <= 2 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 2>, 6);
     else if (a.d <= 5 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 5>, 6);
     else if (a.d <= 9 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 9>, 6);
-    else if (a.d <= 12 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 12>, 6);
+    else if (a.d <= 11 * rms::kGenThreads) any(rms::rms_fwd_any_kernel<XT, YT, 11>, 6);
     else any(rms::rms_fwd_any_kernel<XT, YT, 0>, 8);
     return;
   }
@@ -1484,7 +1484,7 @@ void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t
     if (a.d <= 2 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 2>);
     else if (a.d <= 5 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 5>);
     else if (a.d <= 9 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 9>);
-    else if (a.d <= 12 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 12>);
+    else if (a.d <= 11 * rms::kGenThreads) any(rms::rms_bwd_any_kernel<XT, GT, 11>);
     else any(rms::rms_bwd_any_kernel<XT, GT, 0>);
     return;
   }

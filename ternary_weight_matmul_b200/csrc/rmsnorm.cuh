@@ -6,10 +6,13 @@
 // Bound by HBM: one read of x (and dy), one write of y (dx). A CTA takes R rows at a time with every
 // thread holding the same 8-column chunks of each row in registers, so a row is read once, one block
 // reduction serves R rows, and in the backward the thread's share of dw stays in registers over all
-// rows of the CTA (written once as a partial row, added up in a fixed order by a second kernel).
+// rows of the CTA (written once as a partial row, added up in a fixed order by a second kernel). Rows
+// that 16-byte accesses do not fit (an odd width, an unaligned base) go through kernels that hold single
+// columns in registers instead, up to 11 * 256 of them, and are read twice beyond that or beyond 16384.
 // Sums are float32; y, dx are rounded once to their type. 16384 x 1024 bf16: forward 13.2 us (5.1 TB/s),
-// backward 21.1 + 3.7 us (4.8 TB/s; 39.5 us before the next rows' loads were issued ahead of the block
-// reduction), together 38.7 us of device time against a floor of 25.6.
+// backward 21 + 3.5 us (4.8 TB/s; 39.5 us before the next rows' loads were issued ahead of the block
+// reduction), together 37.5 us of device time against a floor of 25.6. Forward + backward in the same way:
+// 8192 x 2560 bf16 52 us (floor 32), 5001 x 2048 float32 41 (31), 16384 x 2053 bf16 146 (51).
 #pragma once
 
 #include "common.cuh"
@@ -252,8 +255,8 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
 
 // Any width and alignment: single columns, thread t's at t + j * kGenThreads. NC > 0: rows of up to NC *
 // kGenThreads columns, a thread's columns of a row (and its share of dw) in registers, one row at a time
-// so that six CTAs share an SM; NC = 0: wider rows, read twice, dw in the thread's columns of the partial
-// row.
+// so that four to six CTAs share an SM (16384 x 2053 bf16, forward + backward: 146 us against 190 for the
+// form that reads twice); NC = 0: wider rows, read twice, dw in the thread's columns of the partial row.
 template <mmf_dtype DT>
 __device__ __forceinline__ float at(const void* p, int64_t i) {
   return Elem<DT>::load(reinterpret_cast<const typename Elem<DT>::T*>(p) + i);

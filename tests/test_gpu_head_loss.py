@@ -426,6 +426,19 @@ def test_norm_shapes_and_types(mmf, shape, xt, gt, yt):
     check_norm(mmf, x, None, dy, 1e-2)
 
 
+# more rows than one turn of all CTAs takes, at every number of rows a turn and on both sides of the widths
+# where an odd row moves to the next kernel
+@pytest.mark.parametrize("xt,gt", [(BF16, BF16), (F32, F32), (BF16, F32)])
+@pytest.mark.parametrize("m,d", [(8005, 200), (5003, 512), (4001, 1024), (2503, 1536), (1501, 2560), (1203, 8192),
+                                 (2003, 511), (1999, 513), (2001, 1279), (1501, 1281), (1507, 2303), (1201, 2305),
+                                 (1203, 2815), (1205, 2817)])
+def test_norm_of_many_turns(mmf, m, d, xt, gt):
+    g = gen(m + d)
+    x = (torch.randn(m, 1, generator=g, device=DEV).exp() * torch.randn(m, d, generator=g, device=DEV)).to(xt)
+    dy = torch.randn(m, d, generator=g, device=DEV).to(gt)
+    check_norm(mmf, x, 1 + 0.2 * torch.randn(d, generator=g, device=DEV), dy, 1e-8)
+
+
 def test_norm_unaligned_rows_zero_rows_and_no_rows(mmf):
     g = gen(3)
     flat = torch.randn(40 * 64 + 1, generator=g, device=DEV)
