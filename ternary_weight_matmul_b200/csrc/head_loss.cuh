@@ -50,6 +50,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "pair_exit.cuh"
 
 namespace mmf {
 namespace hl {
@@ -174,11 +175,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// shared::cluster address of `bar` in the pair's first CTA
-__device__ __forceinline__ uint32_t in_first_cta(const uint64_t* bar) {
+// shared::cluster address of `p` in the pair's CTA `rank`
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
+}
+__device__ __forceinline__ uint32_t in_first_cta(const uint64_t* bar) { return in_cta(bar, 0); }
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -427,6 +432,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   uint64_t* drain = accempty + 2;            // everything the MMA thread issued
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // by rank, the same in both CTAs: stages the producer issued, with kGaveUp when one of its waits ran out
+  volatile uint32_t* issued = tmem_slot + 2;
+  constexpr uint32_t kGaveUp = 0x80000000u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t limit = P.wait_limit_us;
   const uint32_t rank = cluster_rank();
@@ -462,6 +470,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   const Geo G = geometry<MODE>(P, live);
   const int tiles = G.tiles;
   const int live64 = (live + 63) & ~63;
+  // Fills iteration `it`'s stage with k-block kb of a plane pair; its slot has to be free.
+  const auto fill = [&](const Tile& T, int pa, int pb, int kb, uint32_t it) {
+    const uint32_t s = it % STAGES;
+    const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BOXES * BOX_BYTES;
+    const int k = (T.kb0 + kb) * BK;
+    const uint32_t bar = in_first_cta(&full[s]);
+    const int b_boxes = MODE == kProducts && T.n <= 128 ? 1 : B_BOXES;
+    // kStats reads nothing of the rows past the last: boxes of such rows are left out (a row of A
+    // reaches its own row of D only)
+    int a_boxes = A_BOXES, a_both = 2 * A_BOXES;
+    if (MODE == kStats) {
+      const int left = live - T.row;
+      a_both = left >= BM ? 2 * A_BOXES : (left + 63) >> 6;
+      a_boxes = min(max(a_both - A_BOXES * (int)rank, 0), A_BOXES);
+    }
+    if (rank == 0) mbar_arrive_expect_tx(&full[s], (a_both + 2 * b_boxes) * BOX_BYTES);
+    const int arow = T.row + CM * (int)rank, bcol = T.col + T.n / 2 * (int)rank;
+    if (MODE == kProducts && T.kind == 2) {  // A MN-major, B K-major, k = vocabulary
+#pragma unroll
+      for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.t, arow + 64 * i, P.v0 + k, pb, bar);
+      for (int i = 0; i < b_boxes; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.g, k, bcol + 64 * i, pa, bar);
+    } else if (MODE != kProducts) {
+#pragma unroll
+      for (int i = 0; i < A_BOXES; ++i)
+        if (i < a_boxes) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, arow + 64 * i, pa, bar);
+#pragma unroll
+      for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.t, k, P.v0 + bcol + 64 * i, pb, bar);
+    } else if (T.kind == 0) {  // dT = g^T x: both operands MN-major, k = live rows
+#pragma unroll
+      for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, arow + 64 * i, k, pa, bar);
+#pragma unroll
+      for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.x, bcol + 64 * i, k, pb, bar);
+    } else {  // dx = g T: A K-major, B MN-major, k = vocabulary
+#pragma unroll
+      for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, k, arow + 64 * i, pa, bar);
+#pragma unroll
+      for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.t, bcol + 64 * i, P.v0 + k, pb, bar);
+    }
+  };
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -473,59 +520,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         for (int p = 0; ok && p < T.nprod; ++p) {
           const int pa = pr.a[p], pb = pr.b[p];
           for (int kb = 0; kb < T.nkb; ++kb, ++it) {
-            const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-            if (!mbar_wait_bounded(&empty[s], ph ^ 1u, limit, abort_flag)) { ok = false; break; }
-            const uint32_t sa = smem_u32(smem + s * STAGE_BYTES), sb = sa + A_BOXES * BOX_BYTES;
-            const int k = (T.kb0 + kb) * BK;
-            const uint32_t bar = in_first_cta(&full[s]);
-            const int b_boxes = MODE == kProducts && T.n <= 128 ? 1 : B_BOXES;
-            // kStats reads nothing of the rows past the last: boxes of such rows are left out (a row of A
-            // reaches its own row of D only)
-            int a_boxes = A_BOXES, a_both = 2 * A_BOXES;
-            if (MODE == kStats) {
-              const int left = live - T.row;
-              a_both = left >= BM ? 2 * A_BOXES : (left + 63) >> 6;
-              a_boxes = min(max(a_both - A_BOXES * (int)rank, 0), A_BOXES);
-            }
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], (a_both + 2 * b_boxes) * BOX_BYTES);
-            const int arow = T.row + CM * (int)rank, bcol = T.col + T.n / 2 * (int)rank;
-            if (MODE == kProducts && T.kind == 2) {  // A MN-major, B K-major, k = vocabulary
-#pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.t, arow + 64 * i, P.v0 + k, pb, bar);
-              for (int i = 0; i < b_boxes; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.g, k, bcol + 64 * i, pa, bar);
-            } else if (MODE != kProducts) {
-#pragma unroll
-              for (int i = 0; i < A_BOXES; ++i)
-                if (i < a_boxes) tma_load_3d(sa + i * BOX_BYTES, &P.x, k, arow + 64 * i, pa, bar);
-#pragma unroll
-              for (int i = 0; i < B_BOXES; ++i)
-                tma_load_3d(sb + i * BOX_BYTES, &P.t, k, P.v0 + bcol + 64 * i, pb, bar);
-            } else if (T.kind == 0) {  // dT = g^T x: both operands MN-major, k = live rows
-#pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, arow + 64 * i, k, pa, bar);
-#pragma unroll
-              for (int i = 0; i < B_BOXES; ++i) tma_load_3d(sb + i * BOX_BYTES, &P.x, bcol + 64 * i, k, pb, bar);
-            } else {  // dx = g T: A K-major, B MN-major, k = vocabulary
-#pragma unroll
-              for (int i = 0; i < A_BOXES; ++i) tma_load_3d(sa + i * BOX_BYTES, &P.g, k, arow + 64 * i, pa, bar);
-#pragma unroll
-              for (int i = 0; i < B_BOXES; ++i)
-                tma_load_3d(sb + i * BOX_BYTES, &P.t, bcol + 64 * i, P.v0 + k, pb, bar);
-            }
+            if (!mbar_wait_bounded(&empty[it % STAGES], ((it / STAGES) & 1u) ^ 1u, limit, abort_flag)) { ok = false; break; }
+            fill(T, pa, pb, kb, it);
           }
         }
       }
-      if (ok) {
-        // the last stages' commits have reached this CTA before it ends
-        for (uint32_t j = it > STAGES ? it - STAGES : 0; ok && j < it; ++j)
-          ok = mbar_wait_bounded(&empty[j % STAGES], (j / STAGES) & 1u, limit, abort_flag);
-      }
-      if (!ok && rank == 0) {
-        // drain: the stages armed in the last STAGES iterations must see their copies land (the other
-        // CTA's among them; it cannot end before this one)
-        for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-          mbar_wait_drain(&full[j % STAGES], (j / STAGES) & 1u);
-      }
+      // the last stages' commits have reached this CTA before it ends
+      for (uint32_t j = it > STAGES ? it - STAGES : 0; ok && j < it; ++j)
+        ok = mbar_wait_bounded(&empty[j % STAGES], (j / STAGES) & 1u, limit, abort_flag);
+      for (uint32_t r = 0; r < 2; ++r) st_cluster_u32(in_cta(const_cast<const uint32_t*>(issued) + rank, r), it | (ok ? 0u : kGaveUp));
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -859,6 +862,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
   if (rank == 1 && threadIdx.x == 0) mbar_wait_drain(drain, 0u);
   __syncthreads();
   cluster_sync();
+  if ((issued[0] | issued[1]) & kGaveUp) {  // both CTAs see the same
+    // The producers may have stopped at different iterations. Each issues what only the other one did, so
+    // that every stage's barrier has both CTAs' bytes to come, and the first CTA waits for all of them.
+    if (threadIdx.x == 0) {
+      const PairExit e = pair_exit(issued[rank] & ~kGaveUp, issued[rank ^ 1u] & ~kGaveUp, STAGES);
+      uint32_t it = 0;
+      for (int t = first; it < e.to && t < tiles; t += stride) {
+        const Tile T = tile_at<MODE>(P, G, t);
+        const Prods& pr = MODE != kProducts ? P.fwd : T.kind ? P.dxp : P.dtp;
+        for (int p = 0; p < T.nprod; ++p)
+          for (int kb = 0; kb < T.nkb; ++kb, ++it)
+            if (it >= e.from && it < e.to) fill(T, pr.a[p], pr.b[p], kb, it);
+      }
+      if (rank == 0)
+        for (uint32_t j = e.drain; j < e.to; ++j) mbar_wait_drain(&full[j % STAGES], (j / STAGES) & 1u);
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, TMEM_COLS);
