@@ -32,11 +32,14 @@
 //
 // The tensor cores' float32 accumulator cuts bits off at every step of K = 16, towards zero: a bias of
 // about half an ulp of the running sum per step, 1.3e-6 of logits of size 2 at d = 1024 and 3.8e-6 at
-// 2560 (a float32 sum on the CUDA cores: below 1e-9). Where a result is kept in float32 (the loss
-// statistics, and every gradient with a float32 operand) the kernel therefore starts a new accumulator
-// every FLUSH_KB k-blocks and the epilogue adds the pieces in registers, rounding to nearest. (Relative
-// error of the loss at d = 1024: 1.2e-6 without, 5.6e-7 with 8 k-blocks, 2.6e-7 with 4; of a float32
-// product 4e-7.)
+// 2560 (a float32 sum on the CUDA cores: below 1e-9). For the logits, and for every gradient with a
+// float32 operand, the kernel therefore starts a new accumulator every FLUSH_KB k-blocks and the epilogue
+// adds the pieces in registers, rounding to nearest. (Relative error of the loss at d = 1024: 1.2e-6
+// without, 5.9e-7 with 8 k-blocks, 2.6e-7 with 4; of a float32 product 3.6e-7. With bf16 operands 4 k-blocks
+// cost 9% of forward + backward at 16384 x 1024 against 8.) The backward's logits are added up as the
+// forward's were, to the bit: p = exp(s / tau - lse) sums to one then, whatever s itself is off by, and
+// 1 - p of a row that is sure of its target keeps its digits (before, 1 - p of some 1e-3 at d = 2560 was off
+// by 6% and more; 1% of 16384 x 1024 forward + backward).
 //
 // Measured (32000 words, bf16, back to back): 16384 x 1024 forward + backward 3.53 ms = 1156 TFLOP/s of
 // 8 m vocab d (5% of the rows left out), 0.84 of the sustained cuBLAS rate; 16384 x 2560 6.26 ms = 1200
@@ -102,7 +105,8 @@ struct Params {
   int32_t d, vocab;
   int32_t v0, vn;       // vocabulary range of this launch
   int64_t m_pad;
-  float scale;          // log2(e) / tau
+  float scale;          // log2(e) / tau (kStats)
+  float inv_tau;        // (kGrad)
   const int32_t* tgt;   // [m_pad] target of each live row, or nullptr (kStats, kGrad)
   const float* lse;     // [m_pad] (kGrad)
   const float* c;       // [m_pad] dloss / tau (kGrad)
@@ -417,8 +421,9 @@ __host__ __device__ constexpr int grad_planes(int gp) { return gp == kFine2 ? 2 
 // GP: kGrad's GradPlanes; kStats and kProducts: 1 with bf16 results and operands, else 2.
 template <int MODE, int GP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_loss_kernel(const __grid_constant__ Params P) {
-  constexpr bool FLUSH = MODE == kStats || (GP > 1 && GP != kFine2);
-  constexpr int KB = GP > 1 ? FLUSH_KB_F32 : FLUSH_KB;
+  // kStats and kGrad add up the logits alike, to the bit, so that p = exp(s / tau - lse) fits its lse
+  constexpr bool FLUSH = MODE != kProducts || GP > 1;
+  constexpr int KB = GP > 1 && GP != kFine2 ? FLUSH_KB_F32 : FLUSH_KB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + STAGES * STAGE_BYTES;
@@ -639,7 +644,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           sum[e + 3] *= u.w;
         }
       }
-      const float scale = P.scale * unit;
       // columns [c0, c0 + N) of D into v (with FLUSH they are in `sum` already)
       const auto cols32 = [&](int c0, float* v) {
         uint32_t w[32];
@@ -668,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
         for (int e = 0; e < W; ++e) m4[e & 3] = fmaxf(m4[e & 3], sum[e]);
         const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        const float off = top == -INFINITY ? 0.0f : -top * scale;
+        const float scale = P.scale * unit, off = top == -INFINITY ? 0.0f : -top * scale;
 #pragma unroll
         for (int e = 0; e < W; ++e) s4[e & 3] += ex2(fmaf(sum[e], scale, off));
         if (row < live)
@@ -707,30 +711,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         const bool needed = row0 < live64;  // uniform across the warp
         constexpr bool halves = GP == kHalf2;
         const float c = !needed ? 0.0f : !halves ? P.c[row] : row < live ? kGradUnit : 0.0f;
-        const float lse2 = needed ? P.lse[row] * kLog2e : 0.0f;
+        const float lse = needed ? P.lse[row] : 0.0f, inv_tau = P.inv_tau * unit;
+        // s / tau - lse before the change of base: where p is near 1 it is a small difference, exact but for lse
+        const auto prob = [&](float sv) { return ex2(fmaf(sv, inv_tau, -lse) * kLog2e); };
         const int tgt = needed && P.tgt ? P.tgt[row] - P.v0 - col0 : -1;
-        const auto grads = [&](float* gv, int c0, int w) {
+        if (needed && grad_planes(GP) != 2) {
 #pragma unroll
-          for (int e = 0; e < w; ++e) gv[e] = ex2(fmaf(gv[e], scale, -lse2));
-          if ((uint32_t)(tgt - c0) < (uint32_t)w) {
+          for (int e = 0; e < BN / 2; ++e) sum[FLUSH ? e : 0] = prob(sum[FLUSH ? e : 0]);
+          if ((uint32_t)tgt < (uint32_t)(BN / 2)) {
 #pragma unroll
-            for (int e = 0; e < w; ++e)
-              if (tgt - c0 == e) gv[e] -= 1.0f;
+            for (int e = 0; e < BN / 2; ++e)
+              if (tgt == e) sum[FLUSH ? e : 0] -= 1.0f;
           }
 #pragma unroll
-          for (int e = 0; e < w; ++e) gv[e] *= c;
-        };
-        if (FLUSH && needed && grad_planes(GP) != 2) grads(sum, 0, FLUSH ? BN / 2 : 0);
+          for (int e = 0; e < BN / 2; ++e) sum[FLUSH ? e : 0] *= c;
+        }
 #pragma unroll
         for (int c0 = 0; c0 < BN / 2; c0 += 64) {
           if (!needed || col0 + c0 >= P.vn) break;
-          float own[FLUSH ? 1 : 64];
-          float* gv = FLUSH ? sum + (FLUSH ? c0 : 0) : own;
-          if (!FLUSH) {
-            cols32(c0, gv);
-            cols32(c0 + 32, gv + 32);
-            if (grad_planes(GP) != 2) grads(gv, c0, FLUSH ? 0 : 64);
-          }
+          float* gv = sum + (FLUSH ? c0 : 0);
           if (grad_planes(GP) == 2) {
             // both planes at once, one per buffer: a value is worked out, split and gone
             if (lane == 0) bulk_wait_read<0>();
@@ -741,7 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int e = 8 * j + 2 * q;
-                float a = ex2(fmaf(gv[e], scale, -lse2)), b = ex2(fmaf(gv[e + 1], scale, -lse2));
+                float a = prob(gv[e]), b = prob(gv[e + 1]);
                 if (tgt - c0 == e) a -= 1.0f;
                 if (tgt - c0 == e + 1) b -= 1.0f;
                 a *= c;
@@ -774,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
                   float& b = gv[8 * j + 2 * q + 1];
                   // keeps the compiler from splitting all values ahead of the stores, into spills
                   asm volatile("" : "+f"(a), "+f"(b));
-                  w[q] = !FLUSH ? pack_bf16_rn(a, b) : pack_bf16_hi(peel(a), peel(b));
+                  w[q] = GP == kOne ? pack_bf16_rn(a, b) : pack_bf16_hi(peel(a), peel(b));
                 }
                 st_shared_v4(stg_row + (((uint32_t)j << 4) ^ swz), w[0], w[1], w[2], w[3]);
               }

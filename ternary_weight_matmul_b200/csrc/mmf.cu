@@ -1289,6 +1289,7 @@ mmf_status loss_rows(const LossArgs& a, const LossPlan& L, hl::GatherArgs ga, fl
   P.vocab = a.vocab;
   P.m_pad = L.m_pad;
   P.scale = hl::kLog2e / a.tau;
+  P.inv_tau = 1.0f / a.tau;
   P.fwd = loss_prods(L.px, L.pt, a.tdt == MMF_F32 ? 1 : 2);
   P.wait_limit_us = g_wait_limit.load();
   return MMF_OK;

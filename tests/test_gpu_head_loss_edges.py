@@ -39,3 +39,70 @@ def test_waits_that_run_out_end_in_order(mmf, m, d, v):  # noqa: F811
         assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert mmf.sync_status(DEV) == mmf.MMF_OK
+
+
+def confident(m, d, v, gap, tau=1.0):
+    """Rows whose target stands about `gap` above the other words, whose logits are near 17 tau:
+    sums of d terms of one sign, which is where an accumulator that cuts bits off drifts. Column 0 of x is
+    zero and of the table 8, so that it takes no part in the logits and dx[:, 0] = 8 sum_v g_rv."""
+    g = gen(m + v)
+    shared = torch.randn(d, generator=g, device=DEV)
+    x = (0.7 * shared + 0.7 * torch.randn(m, d, generator=g, device=DEV)).to(BF16)
+    x[:, 0] = 0
+    targets = torch.randperm(v, generator=g, device=DEV)[:m].to(torch.int32)
+    t = (17 * tau / 0.7 / d) * shared + (0.3 * tau / math.sqrt(d)) * torch.randn(v, d, generator=g, device=DEV)
+    t[targets.long()] += gap * tau / 0.49 / d * (x.float() - 0.7 * shared)
+    t = t.to(BF16)
+    t[:, 0] = 8.0
+    return x, t, targets, g
+
+
+def row_errors(x, t, q, tau):
+    """float64 p, and bounds on the kernels' relative error of p and absolute error near p = 1 per row: the
+    same sums s enter lse and p, whose errors (16 steps of at most u of a piece's sum, added rounding to
+    nearest: 32 u max |s| / tau with either sign) cancel in the row's total but not between words; what is
+    left on p itself is lse's last bit (half of 2^-23 of 2^floor(log2 |lse|) at most u |lse|), the sum's and
+    exponentials' 16 u, and the product with 1 / tau, u |s| / tau."""
+    s = x.double() @ t.double().T / tau
+    lse = torch.logsumexp(s, 1)
+    p = torch.exp(s - lse[:, None])
+    words = 64 * U * s.abs().max(1).values
+    level = U * (16 + 2 * lse.abs())
+    if tau != 1.0:
+        level = level + 2 * U * s.abs().max(1).values
+    return p, p - q, words, level
+
+
+@pytest.mark.parametrize("m", [100, 200, 700])
+@pytest.mark.parametrize("gap", [13.0, 14.5])
+def test_xent_gradient_of_confident_rows(mmf, m, gap):  # noqa: F811
+    d, v = 2560, 1000
+    x, t, targets, g = confident(m, d, v, gap)
+    dloss = 1 + torch.rand(m, generator=g, device=DEV)
+    q = torch.zeros(m, v, dtype=torch.float64, device=DEV).scatter_(1, targets.long()[:, None], 1.0)
+    p, gv, words, level = row_errors(x, t, q, 1.0)
+    assert ((p * q).sum(1) > 0.98).all() and ((p * q).sum(1) < 0.99999).all()
+    _, lse = mmf.lm_head_xent_fwd(x, t, targets)
+    dx, _ = mmf.lm_head_xent_backward(x, t, targets, lse, dloss)
+    c = dloss.double()[:, None]
+    T = t.double()
+    want = c * (gv @ T)
+    # row by row in the 2-norm: g's and dx's roundings to bf16, the words' errors on the off-target part and
+    # the level's on all of p; products of V / 16 steps
+    size = c * (gv.abs() @ T.norm(dim=1)[:, None])
+    tol = (2 * h(BF16) + 3 * words[:, None] + (v / 16 + 64) * U) * size + level[:, None] * c * (p @ T.norm(dim=1)[:, None])
+    off = (dx.double() - want).norm(dim=1, keepdim=True)
+    assert (off <= tol).all(), float((off / tol).max())
+    check_zero_sum(dx, c, p, gv, words, level, m)
+    assert mmf.sync_status(DEV) == mmf.MMF_OK
+
+
+def check_zero_sum(dx, c, p, gv, words, level, m):
+    """dx[:, 0] = 8 sum_v g_rv = 0: what is left is each g's rounding (up to 128 rows two bf16 values,
+    2^-16 of it, else one, 2^-8), the level's error of p, and 3 V / 16 steps of u of the products' sums."""
+    v = p.shape[1]
+    planes = 2.0 ** -16 if m <= 128 else 2.0 ** -8
+    tol = 8 * c[:, 0] * ((planes + 3 * (v / 16 + 8) * U + 2.0 ** -16) * gv.abs().sum(1) + level * p.sum(1)
+                         + words * (1 - p.max(1).values))
+    off = dx[:, 0].double().abs()
+    assert (off <= tol).all(), float((off / tol).max())
