@@ -106,3 +106,41 @@ def check_zero_sum(dx, c, p, gv, words, level, m):
                          + words * (1 - p.max(1).values))
     off = dx[:, 0].double().abs()
     assert (off <= tol).all(), float((off / tol).max())
+    return tol
+
+
+def check_one_value_misses(c, gv, tol):
+    """The same sums with every g rounded to one bf16 value, in float64: most rows are out of the bound."""
+    once = 8 * (c * gv).to(BF16).double().sum(1).abs()
+    assert (once > tol).double().mean() > 0.8, float((once / tol).median())
+
+
+@pytest.mark.parametrize("m", [1, 100, 128, 129])
+@pytest.mark.parametrize("tau", [1.0, 2.0])
+def test_gradient_rows_sum_to_zero(mmf, m, tau):  # noqa: F811
+    """Ordinary rows: g is of order one at the targets and the teacher's entries, whose roundings lead. Up to
+    128 rows they are held in two bf16 values, which one value would miss by two orders."""
+    d, v, k = 256, 1000, 6
+    x, t, g = operands(81 + m, m, d, v, BF16, BF16)
+    x[:, 0], t[:, 0] = 0, 8.0
+    c = 1 + torch.rand(m, generator=g, device=DEV)
+    if tau == 1.0:
+        targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
+        q = torch.zeros(m, v, dtype=torch.float64, device=DEV).scatter_(1, targets.long()[:, None], 1.0)
+        p, gv, words, level = row_errors(x, t, q, 1.0)
+        _, lse = mmf.lm_head_xent_fwd(x, t, targets)
+        dx, _ = mmf.lm_head_xent_backward(x, t, targets, lse, c)
+        tol = check_zero_sum(dx, c.double()[:, None], p, gv, words, level, m)
+        if 1 < m <= 128:
+            check_one_value_misses(c.double()[:, None], gv, tol)
+    ids = torch.stack([torch.randperm(v, generator=g, device=DEV)[:k] for _ in range(m)]).to(torch.int32)
+    logits = 2 * torch.randn(m, k, generator=g, device=DEV)
+    w = torch.softmax(logits.double() / tau, 1)
+    q = torch.zeros(m, v, dtype=torch.float64, device=DEV).scatter_(1, ids.long(), w)
+    p, gv, words, level = row_errors(x, t, q, tau)
+    _, lse, s_top = mmf.lm_head_distill_fwd(x, t, ids, logits, temperature=tau)
+    dx, _ = mmf.lm_head_distill_backward(x, t, ids, logits, lse, s_top, c, temperature=tau)
+    tol = check_zero_sum(dx, c.double()[:, None] / tau, p, gv, words, level + 64 * U, m)
+    if 1 < m <= 128:
+        check_one_value_misses(c.double()[:, None] / tau, gv, tol)
+    assert mmf.sync_status(DEV) == mmf.MMF_OK
