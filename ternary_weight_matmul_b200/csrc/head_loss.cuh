@@ -626,22 +626,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
         for (int e = 0; e < (FLUSH ? BN / 2 : 1); ++e) sum[e] = 0.0f;
       }
       // the powers of two of fp16 operands: of the row and the table, or of dT's (dx's go where its
-      // partials are added)
+      // partials are added). A product of two that is past the range belongs to logits that are zero, or past
+      // it too
       float unit = 1.0f;
       if (FLUSH && P.x_unit)
         unit = MODE == kStats   ? (row < live ? P.x_unit[row] : 0.0f)
-               : MODE == kGrad  ? (row < live ? P.x_unit[row] * *P.t_unit : 0.0f)
+               : MODE == kGrad  ? (row < live ? fminf(P.x_unit[row] * *P.t_unit, 3.402823466e38f) : 0.0f)
                : T.kind == 0    ? *P.dt_unit * (1.0f / kGradUnit)
                                 : 1.0f;
       if (MODE == kStats && GP > 1 && P.t_units) {
+        // s from the raw sum (2^45 at most): the smaller power first, so that a row of 2^-120 beside a word of
+        // 2^120 stays in range on the way (what the sum loses below 2^-126 is 2^-36 of such a logit at most)
+        const auto scaled = [&](float v, float u) { return v * fminf(unit, u) * fmaxf(unit, u); };
         const float4* u4 = reinterpret_cast<const float4*>(P.t_units + col0);  // one address for the warp
 #pragma unroll
         for (int e = 0; e < (FLUSH ? BN / 2 : 0); e += 4) {
           const float4 u = u4[e / 4];
-          sum[e] *= u.x;
-          sum[e + 1] *= u.y;
-          sum[e + 2] *= u.z;
-          sum[e + 3] *= u.w;
+          sum[e] = scaled(sum[e], u.x);
+          sum[e + 1] = scaled(sum[e + 1], u.y);
+          sum[e + 2] = scaled(sum[e + 2], u.z);
+          sum[e + 3] = scaled(sum[e + 3], u.w);
         }
       }
       // columns [c0, c0 + N) of D into v (with FLUSH they are in `sum` already)
@@ -666,17 +670,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
 #pragma unroll
           for (int e = 0; e < W; ++e)
             if (tgt == (uint32_t)e) hit = sum[e];
-          P.st[row] = hit * unit;
+          P.st[row] = hit;
         }
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int e = 0; e < W; ++e) m4[e & 3] = fmaxf(m4[e & 3], sum[e]);
         const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        const float scale = P.scale * unit, off = top == -INFINITY ? 0.0f : -top * scale;
+        const float scale = P.scale, off = top == -INFINITY ? 0.0f : -top * scale;
 #pragma unroll
         for (int e = 0; e < W; ++e) s4[e & 3] += ex2(fmaf(sum[e], scale, off));
         if (row < live)
-          P.part[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + row] = make_float2(top * unit, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+          P.part[(int64_t)((T.col / BN) * 2 + half) * P.m_pad + row] = make_float2(top, (s4[0] + s4[1]) + (s4[2] + s4[3]));
         if (P.top) {
           // the logits at the teacher's ids, while they are here: a group of 32 columns that holds one
           // of the warp's entries goes through the warp's staging rows, where it can be indexed
@@ -700,7 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
                            __float_as_uint(sum[FLUSH ? c0 + 4 * j + 3 : 0]));
             while (ent.x < begin + 32) {  // at most top_k entries; a row reads what its own thread wrote
               const uint32_t c = (uint32_t)(ent.x - begin);
-              P.s_top[base + ent.y] = unit * ld_shared_f32(stg_row + (((c >> 2) << 4) ^ swz) + ((c & 3u) << 2));
+              P.s_top[base + ent.y] = ld_shared_f32(stg_row + (((c >> 2) << 4) ^ swz) + ((c & 3u) << 2));
               ent = ++pos < P.top_k ? P.top[base + pos] : make_int2(0x7fffffff, 0);
             }
           }
@@ -1017,7 +1021,7 @@ __device__ __forceinline__ void place_row(const GatherArgs& a, int64_t i, int64_
     }
     if (lane == 0) {
       a.x_unit[i] = 1.0f / up;
-      if (a.row_most) a.row_most[i] = finite_abs(most * a.dloss[r] * a.inv_tau);
+      if (a.row_most) a.row_most[i] = finite_abs(most * (a.dloss[r] * a.inv_tau));
     }
   } else {
     for (int c = lane; c < nck; c += 32) {
@@ -1318,9 +1322,10 @@ __global__ void __launch_bounds__(kRowThreads) join_planes_kernel(const float* _
     }
     const int64_t r = rowmap ? rowmap[i] : i;
     if (c_p) {
-      const float u = *unit * (1.0f / kGradUnit), c = c_p[i];
+      // in 64 bits: the unit and c may leave float32's range one after the other, in either order
+      const double u = (double)*unit * (1.0f / kGradUnit) * c_p[i];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * u * c;
+      for (int e = 0; e < 8; ++e) v[e] = (float)(v[e] * u);
     }
     if (OT == MMF_F32) {
       float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + r * d) + 2 * c;

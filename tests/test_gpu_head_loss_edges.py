@@ -6,7 +6,8 @@ import time
 import pytest
 import torch
 
-from test_gpu_head_loss import BF16, DEV, F32, gen, h, mmf, operands  # noqa: F401
+from test_gpu_head_loss import (BF16, DEV, F32, check_distill, check_xent, gen, h, mmf, operands,  # noqa: F401
+                                teacher)
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -23
@@ -144,3 +145,40 @@ def test_gradient_rows_sum_to_zero(mmf, m, tau):  # noqa: F811
     if 1 < m <= 128:
         check_one_value_misses(c.double()[:, None] / tau, gv, tol)
     assert mmf.sync_status(DEV) == mmf.MMF_OK
+
+
+@pytest.mark.parametrize("m", [90, 900])
+@pytest.mark.parametrize("up", [1e34, 1e36, 1e-34, 1e-36])
+def test_float32_ends_of_the_range(mmf, m, up):  # noqa: F811
+    """Rows of 1e-36 beside a table of 1e36 and the other way round, logits of order one to ten."""
+    x, t, g = operands(91, m, 128, 600, F32, F32)
+    x[3] *= 1e-2
+    targets = torch.randint(0, 600, (m,), generator=g, device=DEV).to(torch.int32)
+    assert float((x @ t.T).abs().max()) > 4
+    check_xent(mmf, x * up, t / up, targets, torch.randn(m, generator=g, device=DEV))
+    ids, logits, dloss = teacher(92, m, 7, 600, F32)
+    check_distill(mmf, x * up, t / up, ids, logits, 2.0, dloss)
+
+
+@pytest.mark.parametrize("m", [90, 900])
+def test_float32_far_magnitudes_of_table_and_dloss(mmf, m):  # noqa: F811
+    """dloss takes back what the table is away from one: dx of order one from a table of 1e-36 and dloss of
+    1e30, and of 1e36 and 1e-30; c x is what has to stay in range for dtable."""
+    x, t, g = operands(93, m, 128, 600, F32, F32)
+    targets = torch.randint(0, 600, (m,), generator=g, device=DEV).to(torch.int32)
+    dloss = torch.randn(m, generator=g, device=DEV)
+    check_xent(mmf, x, t * 1e-36, targets, dloss * 1e30)
+    check_xent(mmf, x * 1e-36, t * 1e36, targets, dloss * 1e-30, (True, False))
+    # |x| |dloss| is past the range, its share at temperature 1000 is not
+    ids, logits, dloss = teacher(94, m, 7, 600, F32)
+    check_distill(mmf, x * 1e20, t * 1e-20, ids, logits, 1000.0, (1 + dloss.abs()) * 1e18)
+
+
+def test_float32_zero_products_of_far_operands(mmf):  # noqa: F811
+    """Rows and words of 1e30 that share no column: every logit is zero, as in float32."""
+    m, d, v = 40, 64, 300
+    x, t, g = operands(95, m, d, v, F32, F32)
+    x, t = x * 1e30, t * 1e30
+    x[:, 32:], t[:, :32] = 0, 0
+    targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
+    check_xent(mmf, x, t, targets, torch.rand(m, generator=g, device=DEV))
