@@ -315,8 +315,10 @@ mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int
  * dloss = 1 / rows):  g_rv = dloss[r] (exp(s_rv - lse[r]) - [v = targets[r]])
  *   dx = g table          [m][d] x_dtype out or NULL, 16-byte aligned (zero in rows left out)
  *   dtable = g^T x        [vocab][d] table_dtype out or NULL, 16-byte aligned (every row written)
- * The logits are computed again in pieces of the vocabulary; one piece's g is held in the workspace
- * (about 512 MB at most up to 65536 rows). g is rounded to bf16 once where x and table are bf16 (held in
+ * The logits are computed again in pieces of the vocabulary; the workspace holds one piece's g (512 MB at most
+ * up to 65536 rows with bf16 operands, 21845 to 32768 with a float32 one; beyond, the rows times 4096 words), the
+ * live rows, dx in float32 (and where few tiles would leave the GPU idle, some tens of MB of partials), and with a
+ * float32 table its two planes: 0.6 GiB at 16384 x 1024 bf16, 1.4 at 65536 x 2560, for any vocabulary. g is rounded to bf16 once where x and table are bf16 (held in
  * two bf16 values up to 128 rows); with float32 rows beside a bf16 table it is kept exactly, and with a
  * float32 table g / dloss to 2^-22, or 2^-39 where it is below 2^-17. Products accumulate in float32.
  * Deterministic; no output may alias an input.

@@ -98,7 +98,7 @@ struct Params {
   CUtensorMap g;    // the piece's g       [pg][m_pad][ldg], inner extent = piece columns; one plane
                     // rounded to nearest, three that split it exactly, or (fp16) two of g / c
   CUtensorMap g_out;   // the same array, box 64 x 32 (stores)
-  CUtensorMap dx_out;  // float32 partials [planes][m_pad][d], box 32 x 32
+  CUtensorMap dx_out;  // float32 partials [splits][m_pad][d], box 32 x 32
   CUtensorMap dt_out;  // dtable's rows of the piece (its dtype), or float32 partials [planes][vocab][d]
   const int32_t* live;  // device: live rows; nullptr: rows of the caller's x, taken as they are (kStats)
   int32_t rows;
@@ -119,7 +119,8 @@ struct Params {
   float* s_top;         // [m][top_k] out: the student's logits at the entries
   int32_t top_k;
   Prods fwd, dxp, dtp;
-  int32_t dx_split, dx_plane0;  // K splits of dx in this launch (0: no dx) and its first partial plane
+  int32_t dx_split;             // K splits of dx in this launch (0: no dx)
+  int32_t dx_add;               // a later piece: dx's partials are added to
   int32_t dt_split;             // K splits of dT (0: no dT)
   int32_t dt_f32;               // dt_out holds float32
   // float32 tables (fp16 planes): the powers of two to take out, else nullptr
@@ -150,6 +151,13 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(src)
+               : "memory");
+}
+// The same, added to what is there (float32).
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(c0), "r"(c1), "r"(c2), "r"(src)
                : "memory");
@@ -794,7 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
       } else if (T.kind == 2) {
         // lane = column of d, column = row: a row's 32 values leave as 128 bytes
         const int dcol = T.row + CM * (int)rank + quarter * 32 + lane;
-        float* o = P.dx_part + ((int64_t)(P.dx_plane0 + T.split) * P.m_pad + col0) * P.d + dcol;
+        float* o = P.dx_part + ((int64_t)T.split * P.m_pad + col0) * P.d + dcol;
 #pragma unroll
         for (int c0 = 0; c0 < BN / 2; c0 += 32) {
           if (c0 >= nh || col0 + c0 >= live) break;
@@ -803,13 +811,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
           if (!FLUSH) cols32(c0, v);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (dcol < P.d && col0 + c0 + e < live) o[(int64_t)(c0 + e) * P.d] = v[e];
+            if (dcol < P.d && col0 + c0 + e < live) {
+              float* at = o + (int64_t)(c0 + e) * P.d;
+              *at = P.dx_add ? *at + v[e] : v[e];
+            }
         }
       } else {
         const int rows = T.kind ? (int)P.m_pad : P.vn;
         const bool f32 = T.kind || P.dt_f32;
         const CUtensorMap* map = T.kind ? &P.dx_out : &P.dt_out;
-        const int out_row = T.kind ? row0 : P.dt_row0 + row0, plane = T.kind ? P.dx_plane0 + T.split : T.split;
+        const int out_row = T.kind ? row0 : P.dt_row0 + row0;
+        // a value of dx gets one addition per piece, and the pieces are launches in order: the sum is too
+        const bool add = T.kind && P.dx_add;
 #pragma unroll
         for (int c0 = 0; c0 < BN / 2; c0 += 32) {
           if (row0 >= rows || col0 + c0 >= P.d) continue;
@@ -843,7 +856,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) head_los
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(map, stg, col0 + c0 - 32 * h, out_row, plane);
+              if (add) tma_add_3d(map, stg, col0 + c0, out_row, T.split);
+              else tma_store_3d(map, stg, col0 + c0 - 32 * h, out_row, T.split);
               bulk_commit();
             }
             next_buffer();

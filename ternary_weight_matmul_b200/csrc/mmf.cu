@@ -1160,7 +1160,7 @@ LossPlan loss_plan(int64_t m, int32_t d, int32_t vocab, bool xf32, bool tf32, bo
   L.dx_split = loss_splits(L.few_n > 0 ? cdiv64(d, hl::BM) : L.m_pad / hl::BM * nt, L.piece / hl::BK);
   L.dt_split = loss_splits(cdiv64(std::min<int64_t>(L.piece, vocab), hl::BM) * nt, L.m_pad / hl::BK);
   L.g = reinterpret_cast<__nv_bfloat16*>(take((size_t)L.pg * M * L.ldg * 2));
-  L.dxp = reinterpret_cast<float*>(take((size_t)L.pieces * L.dx_split * M * d * 4));
+  L.dxp = reinterpret_cast<float*>(take((size_t)L.dx_split * M * d * 4));
   if (L.dt_split > 1) L.dtp = reinterpret_cast<float*>(take((size_t)L.dt_split * vocab * d * 4));
   L.bytes = off;
   return L;
@@ -1380,7 +1380,7 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
   P.dx_split = dx ? L.dx_split : 0;
   P.dt_split = dtable ? L.dt_split : 0;
   const uint64_t f32row = (uint64_t)a.d * 4, trow = (uint64_t)a.d * dsize(a.tdt);
-  MMF_TRY(encode_3d(&P.dx_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, L.dxp, a.d, L.m_pad, (uint64_t)L.pieces * L.dx_split,
+  MMF_TRY(encode_3d(&P.dx_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, L.dxp, a.d, L.m_pad, (uint64_t)L.dx_split,
                     f32row, L.m_pad * f32row, 32, 32));
   P.dt_f32 = L.dt_split > 1 || a.tdt == MMF_F32;
   if (dtable) {
@@ -1398,7 +1398,7 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
     const uint64_t grow = (uint64_t)L.ldg * 2;
     MMF_TRY(encode_3d(&P.g, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.g, P.vn, L.m_pad, L.pg, grow, L.m_pad * grow, hl::BK, 64));
     MMF_TRY(encode_3d(&P.g_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, L.g, P.vn, L.m_pad, L.pg, grow, L.m_pad * grow, 64, 32));
-    P.dx_plane0 = i * L.dx_split;
+    P.dx_add = i > 0;
     P.dt_row0 = P.v0;
     if (L.gp == hl::kOne) loss_launch<hl::kGrad, hl::kOne>(P, *di, st);
     else if (L.gp == hl::kFine2) loss_launch<hl::kGrad, hl::kFine2>(P, *di, st);
@@ -1425,7 +1425,7 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
       launch_after(hl::join_planes_kernel<MMF_BF16>, dim3(ctas), dim3(hl::kRowThreads), 0, st, part, planes, rows, a.d, count, rows, map, c, unit, out);
     ++launches;
   };
-  if (dx) join(L.dxp, L.pieces * L.dx_split, L.m_pad, L.live, L.rowmap, a.xdt, dx, halves ? L.c : nullptr, L.units);
+  if (dx) join(L.dxp, L.dx_split, L.m_pad, L.live, L.rowmap, a.xdt, dx, halves ? L.c : nullptr, L.units);
   if (dtable && L.dt_split > 1) join(L.dtp, L.dt_split, a.vocab, nullptr, nullptr, a.tdt, dtable, nullptr, nullptr);
   g_launches.fetch_add(launches - 1);  // the timing scope counted one launch itself
   return check_launch("head loss backward kernels");
