@@ -1,7 +1,7 @@
 // rmsnorm.cuh -- K16: RMSNorm on its own (the model's final norm in training) and its gradients.
 //
 //   forward   rho = (mean(x^2) + eps)^(-1/2),  y = x rho w
-//   backward  u = dy w,  dx = rho u - rho^3 x mean(u x),  dw[c] = sum_r dy[r][c] x[r][c] rho_r
+//   backward  u = dy w,  dx = rho u - x rho (rho (rho mean(u x))),  dw[c] = sum_r dy[r][c] x[r][c] rho_r
 //
 // Bound by HBM: one read of x (and dy), one write of y (dx). A CTA takes R rows at a time with every
 // thread holding the same 8-column chunks of each row in registers, so a row is read once, one block
@@ -76,9 +76,10 @@ __device__ __forceinline__ void store8(void* p, int64_t idx, const float (&v)[8]
   }
 }
 
-// rho u - k x, with its roundings spelled out: the compiler may otherwise pick either product for the fused
-// one, here this and there that, and dx would depend on whether dw is asked for
-__device__ __forceinline__ float grad(float rho, float u, float k, float x) { return fmaf(-k, x, __fmul_rn(rho, u)); }
+// dx = rho u - k xh with xh = x rho and k = rho (rho mean(u x)), which is of dx's size: rho^3 alone leaves
+// float32's range for rows of 1e15, or of 1e-13 without eps. The roundings are spelled out, so that dx does not
+// depend on what the compiler fuses where dw is asked for.
+__device__ __forceinline__ float grad(float rho, float u, float k, float xh) { return fmaf(-k, xh, __fmul_rn(rho, u)); }
 
 // Block sums of V values at once; red has V * 16 floats. One barrier before the result; the caller
 // alternates between two red arrays, so that the next call's writes cannot meet this call's reads.
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
     for (int r = 0; r < R; ++r) {
       if (r0 + r >= a.m) continue;
       const float rho = rsqrtf(s[r] * inv_d + a.eps);
-      const float k = rho * rho * rho * (s[R + r] * inv_d);
+      const float k = rho * (rho * (s[R + r] * inv_d));
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int c = j * T + (int)threadIdx.x;
@@ -236,9 +237,9 @@ __global__ void __launch_bounds__(kMaxThreads) rms_bwd_kernel(const Args a) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float xv = raw_at<XT>(x[r][j], e), gv = raw_at<GT>(g[r][j], e);
-          dw[j][e] = fmaf(gv * rho, xv, dw[j][e]);
-          o[e] = grad(rho, gv * w[j][e], k, xv);
+          const float xh = __fmul_rn(raw_at<XT>(x[r][j], e), rho), gv = raw_at<GT>(g[r][j], e);
+          dw[j][e] = fmaf(gv, xh, dw[j][e]);
+          o[e] = grad(rho, gv * w[j][e], k, xh);
         }
         store8<XT>(a.out, (r0 + r) * a.d + 8 * c, o);
       }
@@ -334,18 +335,19 @@ __global__ void __launch_bounds__(kGenThreads, NC > 9 ? 4 : NC > 0 ? 5 : 1) rms_
       }
     block_sums<2>(s, red[turn]);
     const float rho = rsqrtf(s[0] * inv_d + a.eps);
-    const float k = rho * rho * rho * (s[1] * inv_d);
+    const float k = rho * (rho * (s[1] * inv_d));
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = tid + j * kGenThreads;
-      dw[j] = fmaf(g[j] * rho, x[j], dw[j]);
-      if (c < a.d) put<XT>(a.out, r * a.d + c, grad(rho, g[j] * (a.w ? a.w[c] : 1.0f), k, x[j]));
+      const float xh = __fmul_rn(x[j], rho);
+      dw[j] = fmaf(g[j], xh, dw[j]);
+      if (c < a.d) put<XT>(a.out, r * a.d + c, grad(rho, g[j] * (a.w ? a.w[c] : 1.0f), k, xh));
     }
     if (NC == 0)
       for (int c = tid; c < a.d; c += kGenThreads) {
-        const float v = at<XT>(a.x, r * a.d + c), u = at<GT>(a.dy, r * a.d + c);
-        if (part) part[c] = fmaf(u * rho, v, part[c]);
-        put<XT>(a.out, r * a.d + c, grad(rho, u * (a.w ? a.w[c] : 1.0f), k, v));
+        const float xh = __fmul_rn(at<XT>(a.x, r * a.d + c), rho), gv = at<GT>(a.dy, r * a.d + c);
+        if (part) part[c] = fmaf(gv, xh, part[c]);
+        put<XT>(a.out, r * a.d + c, grad(rho, gv * (a.w ? a.w[c] : 1.0f), k, xh));
       }
   }
   if (part) {

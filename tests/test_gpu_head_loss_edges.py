@@ -6,8 +6,8 @@ import time
 import pytest
 import torch
 
-from test_gpu_head_loss import (BF16, DEV, F32, check_distill, check_xent, gen, h, mmf, operands,  # noqa: F401
-                                teacher)
+from test_gpu_head_loss import (BF16, DEV, F32, check_distill, check_norm, check_xent, gen, h, mmf,  # noqa: F401
+                                operands, teacher)
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -23
@@ -193,3 +193,15 @@ def test_few_rows_several_vocabulary_pieces(mmf):  # noqa: F811
     x, t, g = operands(96, m, d, v, BF16, BF16)
     targets = torch.randint(0, v, (m,), generator=g, device=DEV).to(torch.int32)
     check_xent(mmf, x, t, targets, torch.randn(m, generator=g, device=DEV))
+
+
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("d", [1024, 1025, 2817, 9216])
+@pytest.mark.parametrize("size,eps", [(1e15, 1e-8), (1e14, 0.0), (1e-15, 0.0), (1e-13, 0.0), (1e-3, 1e-8)])
+def test_norm_of_rows_far_from_one(mmf, d, size, eps, xt):  # noqa: F811
+    """dy leans towards x, so that the part that the projection takes out is a good share of it; rho^3 alone
+    would leave float32's range."""
+    g = gen(d)
+    n = torch.randn(37, d, generator=g, device=DEV)
+    dy = (n + torch.randn(37, d, generator=g, device=DEV)).to(xt)
+    check_norm(mmf, (size * n).to(xt), 1 + 0.2 * torch.randn(d, generator=g, device=DEV), dy, eps)
