@@ -1490,9 +1490,9 @@ void rms_bwd_launch(const rms::Args& a, const RmsPlan& p, int ctas, cudaStream_t
     return;
   }
   if (p.chunks == 1) {
-    const int rows = rms_bwd_rows(p, XT == MMF_BF16 && GT == MMF_BF16);
-    if (rows == 3) launch_after(rms::rms_bwd_kernel<XT, GT, 1, 3>, grid, dim3(p.threads), 0, st, a);
-    else if (rows == 2) launch_after(rms::rms_bwd_kernel<XT, GT, 1, 2>, grid, dim3(p.threads), 0, st, a);
+    constexpr bool bf16 = XT == MMF_BF16 && GT == MMF_BF16;
+    constexpr int R = bf16 ? 3 : 2;  // what rms_bwd_rows gives where it is not one
+    if (rms_bwd_rows(p, bf16) == R) launch_after(rms::rms_bwd_kernel<XT, GT, 1, R>, grid, dim3(p.threads), 0, st, a);
     else launch_after(rms::rms_bwd_kernel<XT, GT, 1, 1>, grid, dim3(p.threads), 0, st, a);
   }
   else if (p.chunks == 2) launch_after(rms::rms_bwd_kernel<XT, GT, 2, 1>, grid, dim3(p.threads), 0, st, a);
