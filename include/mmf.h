@@ -279,7 +279,7 @@ mmf_status mmf_lm_head_argmax(const void* x, mmf_dtype x_dtype, int32_t b, int32
 
 /* RMSNorm (the model's final norm, eps 1e-8 as in the blocks; hysenlabs.com block structure):
  *   y = x rho norm_w, rho = (mean(x^2) + eps)^(-1/2)
- *   x [m][d] x_dtype; norm_w [d] float32 or NULL (unit gain); y [m][d] y_dtype; eps >= 0, any d >= 1.
+ *   x [m][d] x_dtype; norm_w [d] float32 or NULL (unit gain); y [m][d] y_dtype; eps >= 0, 1 <= d <= 2^30.
  * Float32 sums (a row's sum of squares has to be a finite float32), one rounding to y's type. Rows with
  * 16-byte aligned buffers and d a multiple of 8 up to 16384 are read once, 16 bytes at a time; others one
  * value at a time, once for d up to 2816, twice beyond. m = 0 is a no-op. */
@@ -288,7 +288,8 @@ mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t 
 
 /* Its gradients: u = dy norm_w, dx = rho u - rho^3 x mean(u x), dnorm_w[c] = sum_r dy[r][c] x[r][c] rho_r.
  *   x [m][d] x_dtype; dy [m][d] dy_dtype; dx [m][d] x_dtype out; dnorm_w [d] float32 out or NULL.
- *   ws >= mmf_workspace_bytes(MMF_OP_RMSNORM_BWD, m, d, 0, 0) when dnorm_w is asked for.
+ *   ws >= mmf_workspace_bytes(MMF_OP_RMSNORM_BWD, m, d, 0, 0) when dnorm_w is asked for (a float32 row per CTA,
+ *   no more than m).
  * Float32 sums in a fixed order (deterministic). m = 0 writes a zero dnorm_w. dx may not alias an input. */
 mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
                                 const void* dy, mmf_dtype dy_dtype, void* dx, float* dnorm_w, void* ws,

@@ -647,7 +647,7 @@ def rmsnorm_backward(x: torch.Tensor, norm_w: torch.Tensor | None, dy: torch.Ten
     dx = torch.empty_like(x)
     dnw = torch.empty(d, dtype=torch.float32, device=x.device) if want_dnorm_w else None
     with _on(x.device):
-        ws = _scratch(MMF_OP_RMSNORM_BWD, m, d, 0, 0, x.device)
+        ws = _scratch(MMF_OP_RMSNORM_BWD, m if want_dnorm_w else 0, d, 0, 0, x.device)
         _check(lib().mmf_rmsnorm_backward(x.data_ptr(), _dt(x.dtype), m, d, _ptr(norm_w), eps, dy.data_ptr(),
                                           _dt(dy.dtype), dx.data_ptr(), _ptr(dnw), ws.data_ptr(), ws.numel(),
                                           _stream(x.device)), "mmf_rmsnorm_backward")

@@ -1434,8 +1434,10 @@ mmf_status loss_backward(const LossArgs& a, const float* lse, const float* s_top
 // ---------------------------------------------------------------------------------------------
 // RMSNorm
 // ---------------------------------------------------------------------------------------------
-// Partial rows of the gain's gradient (CTAs of the backward): narrow rows take small CTAs, so more of them.
-int64_t rms_max_parts(int32_t d) { return d <= 512 ? 2048 : 1024; }
+constexpr int32_t kRmsMaxD = 1 << 30;
+// Partial rows of the gain's gradient (CTAs of the backward, one row each at least): narrow rows take small
+// CTAs, so more of them.
+int64_t rms_max_parts(int64_t m, int32_t d) { return std::min<int64_t>(m, d <= 512 ? 2048 : 1024); }
 
 // Rows per CTA turn, and the vector kernels' shape: threads x chunks cover d / 8.
 struct RmsPlan {
@@ -1580,7 +1582,7 @@ size_t mmf_workspace_bytes(mmf_op op, int64_t m, int32_t d, int32_t inner, int32
     case MMF_OP_HEAD:
       return inner > 0 ? head_ws_bytes(inner, d) : 0;
     case MMF_OP_RMSNORM_BWD:
-      return align256((size_t)rms_max_parts(d) * d * sizeof(float));
+      return align256((size_t)rms_max_parts(m, d) * d * sizeof(float));
     case MMF_OP_HEAD_LOSS:
     case MMF_OP_HEAD_LOSS_BWD:
       return d > 0 && inner > 0 ? loss_plan(m, d, inner, (n_layers & 1) != 0, (n_layers & 2) != 0,
@@ -2458,7 +2460,7 @@ mmf_status mmf_hgrn2_recurrence(const void* q, const void* f, const void* i, mmf
 // ---------------------------------------------------------------------------------------------
 mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
                            void* y, mmf_dtype y_dtype, mmf_stream_t stream) {
-  MMF_CHECK_ARG(m >= 0 && d > 0, "rmsnorm: bad sizes m=%lld d=%d", (long long)m, d);
+  MMF_CHECK_ARG(m >= 0 && d > 0 && d <= kRmsMaxD, "rmsnorm: bad sizes m=%lld d=%d", (long long)m, d);
   MMF_CHECK_ARG(valid_dtype(x_dtype) && valid_dtype(y_dtype), "rmsnorm: bad dtype");
   MMF_CHECK_ARG(eps >= 0.0f, "rmsnorm: negative eps");
   if (m == 0) return MMF_OK;
@@ -2484,7 +2486,7 @@ mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t 
 mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
                                 const void* dy, mmf_dtype dy_dtype, void* dx, float* dnorm_w, void* ws,
                                 size_t ws_bytes, mmf_stream_t stream) {
-  MMF_CHECK_ARG(m >= 0 && d > 0, "rmsnorm backward: bad sizes m=%lld d=%d", (long long)m, d);
+  MMF_CHECK_ARG(m >= 0 && d > 0 && d <= kRmsMaxD, "rmsnorm backward: bad sizes m=%lld d=%d", (long long)m, d);
   MMF_CHECK_ARG(valid_dtype(x_dtype) && valid_dtype(dy_dtype), "rmsnorm backward: bad dtype");
   MMF_CHECK_ARG(eps >= 0.0f, "rmsnorm backward: negative eps");
   MMF_CHECK_ARG(m == 0 || (x && dy && dx), "rmsnorm backward: null pointer");
@@ -2505,7 +2507,7 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
   const RmsPlan p = rms_plan(d, {x, dy, dx, norm_w});
   const int rows = rms_bwd_rows(p, x_dtype == MMF_BF16 && dy_dtype == MMF_BF16);
   const int ctas = (int)std::min<int64_t>({(m + rows - 1) / rows, (int64_t)di->sms * (!p.vec ? 5 : p.threads <= 64 ? 12 : 4),
-                                           rms_max_parts(d)});
+                                           rms_max_parts(m, d)});
   if (x_dtype == MMF_F32) {
     if (dy_dtype == MMF_F32) rms_bwd_launch<MMF_F32, MMF_F32>(a, p, ctas, st);
     else rms_bwd_launch<MMF_F32, MMF_BF16>(a, p, ctas, st);

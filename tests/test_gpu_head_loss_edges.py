@@ -205,3 +205,28 @@ def test_norm_of_rows_far_from_one(mmf, d, size, eps, xt):  # noqa: F811
     n = torch.randn(37, d, generator=g, device=DEV)
     dy = (n + torch.randn(37, d, generator=g, device=DEV)).to(xt)
     check_norm(mmf, (size * n).to(xt), 1 + 0.2 * torch.randn(d, generator=g, device=DEV), dy, eps)
+
+
+def test_norm_of_few_very_wide_rows(mmf):  # noqa: F811
+    """Three rows of five million columns: a thread adds 19532 squares in float32 (half an ulp each at most),
+    the block's tree a few more."""
+    m, d = 3, 5_000_011
+    g = gen(97)
+    x, dy = (torch.randn(m, d, generator=g, device=DEV) for _ in range(2))
+    w = torch.rand(d, generator=g, device=DEV)
+    X, G, W = x.double(), dy.double(), w.double()
+    rel = (d / 256 / 2 + 32) * U
+    rho = (X.square().mean(1, keepdim=True) + 1e-8) ** -0.5
+    y = mmf.rmsnorm_fwd(x, w)
+    assert ((y - X * rho * W).abs() <= rel * (X * rho * W).abs() + 1e-37).all()
+    torch.cuda.reset_peak_memory_stats()
+    start = torch.cuda.memory_allocated()
+    dx, dw = mmf.rmsnorm_backward(x, w, dy)
+    assert torch.cuda.max_memory_allocated() - start < 10 * m * d * 4
+    u = G * W
+    mean = (u * X).mean(1, keepdim=True)
+    want = rho * u - rho ** 3 * X * mean
+    mag = rho * u.abs() + rho ** 3 * X.abs() * (u * X).abs().mean(1, keepdim=True)
+    assert ((dx - want).abs() <= 4 * rel * mag).all()
+    terms = G * X * rho
+    assert ((dw - terms.sum(0)).abs() <= (rel + 8 * U) * terms.abs().sum(0)).all()

@@ -1,8 +1,11 @@
-"""The head losses' workspaces: what the backward holds is one piece of g, the rows and one dx (CPU)."""
+"""The workspaces of the training end (CPU): what the head losses' backward holds is one piece of g, the rows and
+one dx, the RMSNorm backward a row of partial sums per CTA and no more than it has rows."""
 import pytest
+import torch
 
 import ternary_weight_matmul_b200 as mmf
 from ternary_weight_matmul_b200 import build as mbuild
+from test_binding_cpu import fake  # noqa: F401  (fixture)
 
 GIB = 1 << 30
 
@@ -34,3 +37,24 @@ def test_backward_stays_below_the_logits(ws):
     for m, d, v in [(16384, 2560, 32000), (65536, 2048, 32000), (65536, 2560, 32000), (131072, 2560, 32000)]:
         assert ws(mmf.MMF_OP_HEAD_LOSS_BWD, m, d, v, 0) < m * v * 2
     assert ws(mmf.MMF_OP_HEAD_LOSS_BWD, 65536, 2560, 32000, 0) < 2 * GIB
+
+
+def test_norm_backward_holds_no_more_rows_than_it_has(ws, fake):  # noqa: F811
+    op = mmf.MMF_OP_RMSNORM_BWD
+    for d in (8, 512, 513, 16384, 1 << 24, 1 << 30):
+        assert ws(op, 2, d, 0, 0) == (2 * d * 4 + 255) // 256 * 256
+        assert ws(op, 1 << 20, d, 0, 0) == (2048 if d <= 512 else 1024) * d * 4
+    # a call that asks for no dnorm_w takes no scratch for it
+    x = torch.randn(64, 4096)
+    mmf.rmsnorm_backward(x, None, x, want_dnorm_w=False)
+    assert fake.last("mmf_rmsnorm_backward")[11] == 256
+    mmf.rmsnorm_backward(x, None, x)
+    assert fake.last("mmf_rmsnorm_backward")[11] == 64 * 4096 * 4
+
+
+def test_norm_refuses_rows_past_its_index_range():
+    L = mmf.lib()
+    for d in ((1 << 30) + 1, (1 << 31) - 1):
+        assert L.mmf_rmsnorm_fwd(16, 0, 1, d, None, 1e-8, 16, 0, None) == mmf.MMF_ERR_INVALID_ARG
+        assert L.mmf_rmsnorm_backward(16, 0, 1, d, None, 1e-8, 16, 0, 16, None, None, 0,
+                                      None) == mmf.MMF_ERR_INVALID_ARG
