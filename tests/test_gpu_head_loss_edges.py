@@ -230,3 +230,59 @@ def test_norm_of_few_very_wide_rows(mmf):  # noqa: F811
     assert ((dx - want).abs() <= 4 * rel * mag).all()
     terms = G * X * rho
     assert ((dw - terms.sum(0)).abs() <= (rel + 8 * U) * terms.abs().sum(0)).all()
+
+
+def test_offsets_past_32_bits_in_the_table_and_dtable(mmf):  # noqa: F811
+    """2.2 M words of 1024: the last words' elements of the table and of dtable lie past 2^31. The call's
+    rows have their targets among them, and dtable's last rows are those of a call on the last words alone
+    with the same lse (the same tiles' arithmetic)."""
+    m, d, v, tail = 200, 1024, 2_200_064, 512
+    assert (v - tail) * d > 2 ** 31
+    g = gen(98)
+    t = torch.empty(v, d, dtype=BF16, device=DEV)
+    for r in range(0, v, 1 << 19):
+        t[r:r + (1 << 19)] = (torch.randn(min(1 << 19, v - r), d, generator=g, device=DEV) / 32).to(BF16)
+    x = torch.randn(m, d, generator=g, device=DEV).to(BF16)
+    targets = (v - tail + torch.randint(0, tail, (m,), generator=g, device=DEV)).to(torch.int32)
+    loss, lse = mmf.lm_head_xent_fwd(x, t, targets)
+    total = torch.zeros(m, dtype=torch.float64, device=DEV)
+    for r in range(0, v, 1 << 19):
+        total += torch.exp(x.float() @ t[r:r + (1 << 19)].float().T).double().sum(1)   # logits of order one
+    last = slice(v - tail, v)
+    s_t = (x.double() * t[targets.long()].double()).sum(1)
+    assert ((lse - total.log()).abs() <= 1e-4).all()      # the float32 logits' own 1e-5, and v terms in 64 bits
+    assert ((loss - (total.log() - s_t)).abs() <= 1e-4).all()
+    c = torch.rand(m, generator=g, device=DEV)
+    _, dt = mmf.lm_head_xent_backward(x, t, targets, lse, c, want_dx=False)
+    small = t[last].contiguous()
+    _, dt_tail = mmf.lm_head_xent_backward(x, small, (targets - (v - tail)).to(torch.int32), lse, c, want_dx=False)
+    assert dt_tail.any() and torch.equal(dt[last], dt_tail)
+    assert mmf.sync_status(DEV) == mmf.MMF_OK
+
+
+@pytest.mark.parametrize("xt,tt", [(BF16, BF16), (F32, F32)])
+def test_offsets_past_32_bits_in_the_rows_with_dtable(mmf, xt, tt):  # noqa: F811
+    """2.2 M rows of 1024, all but the first and the last hundred left out: dtable and dx of the few live rows,
+    whose elements lie at both ends, are those of a call that has only them."""
+    m, d, v, n = 2_200_000, 1024, 300, 100
+    x, t, g = operands(99, 2 * n, d, v, xt, tt)
+    big = torch.zeros(m, d, dtype=xt, device=DEV)
+    big[:n], big[-n:] = x[:n], x[n:]
+    targets = torch.randint(0, v, (2 * n,), generator=g, device=DEV).to(torch.int32)
+    all_targets = torch.full((m,), -1, dtype=torch.int32, device=DEV)
+    all_targets[:n], all_targets[-n:] = targets[:n], targets[n:]
+    c = torch.rand(2 * n, generator=g, device=DEV)
+    all_c = torch.full((m,), float("nan"), device=DEV)
+    all_c[:n], all_c[-n:] = c[:n], c[n:]
+    loss, lse = mmf.lm_head_xent_fwd(big, t, all_targets)
+    ends = torch.cat([torch.arange(n, device=DEV), torch.arange(m - n, m, device=DEV)])
+    want_loss, want_lse = mmf.lm_head_xent_fwd(x, t, targets)
+    assert torch.equal(loss[ends], want_loss) and torch.equal(lse[ends], want_lse)
+    dx, dt = mmf.lm_head_xent_backward(big, t, all_targets, lse, all_c)
+    want_dx, want_dt = mmf.lm_head_xent_backward(x, t, targets, want_lse, c)
+    # the small call splits its sums over k differently: float32 partials added in another order
+    steps = 64 * U + (2 * h(xt) if xt == BF16 else 0)
+    assert ((dx[ends].double() - want_dx.double()).norm() <= steps * want_dx.double().norm())
+    assert not dx[n:-n].any()
+    assert ((dt.double() - want_dt.double()).norm() <= steps * want_dt.double().norm())
+    assert mmf.sync_status(DEV) == mmf.MMF_OK
