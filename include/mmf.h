@@ -306,8 +306,9 @@ mmf_status mmf_rmsnorm_backward(const void* x, mmf_dtype x_dtype, int64_t m, int
  *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS, m, d, vocab, n_layers as at mmf_op). m = 0 is a no-op.
  * Tensor cores with float32 accumulation (in short runs that are added rounding to nearest) and float32
  * softmax statistics. float32 operands enter as sums of 16-bit values (x beside a bf16 table as three bf16
- * values, exactly; with a float32 table both as two fp16 values under a power of two, to 2^-22), so the
- * results are those of float32 arithmetic. Deterministic; no output may alias an input. */
+ * values, exactly; with a float32 table both as two fp16 values under a power of two: to 2^-22 of a value, or
+ * 2^-39 of the largest one of its row (of 2^-112 at least), whichever is more), so the results are those of
+ * float32 arithmetic. Deterministic; no output may alias an input. */
 mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,
                                 mmf_dtype table_dtype, int32_t vocab, const int32_t* targets, float* loss, float* lse,
                                 void* ws, size_t ws_bytes, mmf_stream_t stream);
@@ -321,7 +322,10 @@ mmf_status mmf_lm_head_xent_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int
  * live rows, dx in float32 (and where few tiles would leave the GPU idle, some tens of MB of partials), and with a
  * float32 table its two planes: 0.6 GiB at 16384 x 1024 bf16, 1.4 at 65536 x 2560, for any vocabulary. g is rounded to bf16 once where x and table are bf16 (held in
  * two bf16 values up to 128 rows); with float32 rows beside a bf16 table it is kept exactly, and with a
- * float32 table g / dloss to 2^-22, or 2^-39 where it is below 2^-17. Products accumulate in float32.
+ * float32 table g / dloss to 2^-22, or 2^-39 where it is below 2^-17. Products accumulate in float32. A
+ * float32 table itself enters the backward to 2^-22 of a value or 2^-39 of the table's largest, and dloss x,
+ * which dtable sums, to 2^-22 or 2^-39 of its largest over all rows: beside an entry 2^21 times larger, 18 bits
+ * are left. p = exp(s - lse) takes lse as it is given, a float32: p's last digits are lse's.
  * Deterministic; no output may alias an input.
  *   ws >= mmf_workspace_bytes(MMF_OP_HEAD_LOSS_BWD, m, d, vocab, n_layers as at mmf_op). m = 0 zeroes dtable. */
 mmf_status mmf_lm_head_xent_backward(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const void* table,

@@ -25,10 +25,11 @@
 // With a float32 table everything is fp16 in two planes instead, hi = fp16(v 2^k), lo = fp16(v 2^k -
 // hi): 11 + 11 bits rounded to nearest, within 2^-22 of v, so three pairs (i + j <= 1; what they drop is
 // 2^-22 too) do what six do in bf16. The power of two keeps fp16's range: one per row for x (taken out
-// in the epilogue), one for the table (the forward: one per row of it), one for c x (c = dloss / tau), which is the rows' side of dT, and
-// 2^15 for g / c = p - teacher, which lies in [-1, 1]. Values below 2^-17 of such a maximum lose bits
-// one by one down to steps of 2^-39 of it: less than float32's rounding of the sums they enter, though
-// not of a single p far below 2^-17.
+// in the epilogue), one for the table (the forward: one per row of it), one for c x (c = dloss / tau),
+// which is the rows' side of dT, and 2^15 for g / c = p - teacher, which lies in [-1, 1]. Values below
+// 2^-17 of such a maximum lose bits one by one down to 2^-39 of it: less than float32's rounding of the
+// sums they enter, though not of a single p far below 2^-17, nor of a row of dtable that only rows of a
+// dloss far below the largest one reach.
 //
 // The tensor cores' float32 accumulator cuts bits off at every step of K = 16, towards zero: a bias of
 // about half an ulp of the running sum per step, 1.3e-6 of logits of size 2 at d = 1024 and 3.8e-6 at
@@ -41,13 +42,15 @@
 // 1 - p of a row that is sure of its target keeps its digits (before, 1 - p of some 1e-3 at d = 2560 was off
 // by 6% and more; 1% of 16384 x 1024 forward + backward).
 //
-// Measured (32000 words, bf16, back to back): 16384 x 1024 forward + backward 3.53 ms = 1156 TFLOP/s of
-// 8 m vocab d (5% of the rows left out), 0.84 of the sustained cuBLAS rate; 16384 x 2560 6.26 ms = 1200
-// (0.87). Alone, 4096 x 1024: statistics 200 us (1340 TFLOP/s), g 204, products 382 (1405); the tensor
-// pipe is active 73 / 71 / 79% of the cycles at 1.6 GHz, TMA loads 10.3 to 11 TB/s out of the L2. What
-// bounds it: shared memory, whose 128 bytes a cycle the MMA's operand reads (64) and the TMA's writes (64)
-// would fill at full rate, and the power cap in long runs. Few rows (40 x 1024): 23 us forward, of which
-// 11 us are the table's 65.5 MB and the rest set-up, HBM's first bytes and the join.
+// Measured (32000 words, bf16, back to back): 16384 x 1024 forward + backward 3.56 ms = 1147 TFLOP/s of
+// 8 m vocab d (5% of the rows left out), 0.83 of the sustained cuBLAS rate; 16384 x 2560 6.3 ms = 1185
+// (0.86). Alone, 4096 x 1024: statistics 206 us (1306 TFLOP/s), g 220 (1222), products 392 (1369); the
+// tensor pipe is active 73 / 66 / 79% of the cycles at 1.6 GHz. No other unit is near its limit: TMA loads
+// 10 TB/s out of the L2 (a third of the crossbar's rate), shared memory's banks 17 to 19% busy reading and
+// as much writing. What is lost: waits between a tile's accumulators, 28 rounds of tiles paid for 27.03,
+// start and end of the launch (6%), and the clock, which the power cap holds below 1.65 GHz. Few rows
+// (40 x 1024): 23 us forward, of which 11 us are the table's 65.5 MB and the rest set-up, HBM's first bytes
+// and the join.
 #pragma once
 
 #include <cuda_fp16.h>
