@@ -280,9 +280,9 @@ mmf_status mmf_lm_head_argmax(const void* x, mmf_dtype x_dtype, int32_t b, int32
 /* RMSNorm (the model's final norm, eps 1e-8 as in the blocks; hysenlabs.com block structure):
  *   y = x rho norm_w, rho = (mean(x^2) + eps)^(-1/2)
  *   x [m][d] x_dtype; norm_w [d] float32 or NULL (unit gain); y [m][d] y_dtype; eps >= 0, 1 <= d <= 2^30.
- * Float32 sums (a row's sum of squares has to be a finite float32), one rounding to y's type. Rows with
- * 16-byte aligned buffers and d a multiple of 8 up to 16384 are read once, 16 bytes at a time; others one
- * value at a time, once for d up to 2816, twice beyond. m = 0 is a no-op. */
+ * Float32 sums (a row's sum of squares has to be a finite float32, and its mean plus eps a normal one), one
+ * rounding to y's type. Rows with 16-byte aligned buffers and d a multiple of 8 up to 16384 are read once, 16
+ * bytes at a time; others one value at a time, once for d up to 2816, twice beyond. m = 0 is a no-op. */
 mmf_status mmf_rmsnorm_fwd(const void* x, mmf_dtype x_dtype, int64_t m, int32_t d, const float* norm_w, float eps,
                            void* y, mmf_dtype y_dtype, mmf_stream_t stream);
 
